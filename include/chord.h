@@ -153,6 +153,50 @@ CHORD_API chord_status_t chord_router_topk_align(const float* logits, int64_t T,
                                                  int32_t* expert_offsets /* [E+1] or NULL */, void* workspace,
                                                  size_t workspace_bytes, chord_stream_t stream);
 
+/* Element types of the entry points that accept several (logits, activations). */
+#define CHORD_DTYPE_F32  0
+#define CHORD_DTYPE_BF16 1
+#define CHORD_DTYPE_F16  2
+
+/* Expert scores of chord_router_scored_align. */
+#define CHORD_SCORE_SOFTMAX 0 /* softmax over the token's unmasked logits */
+#define CHORD_SCORE_SIGMOID 1 /* sigmoid of each logit */
+
+/* ----------------------------------------------------------------------------------
+ * chord_router_scored_align: the router of models that score experts by softmax or
+ * sigmoid, balance them with a bias on the choice and limit a token to a few groups of
+ * experts; fused with the routing sort like chord_router_topk_align (no counterpart on
+ * the pages, which keep routing outside their kernel timings). Per token t, logit l_e:
+ *   s_e = sigmoid(l_e), or softmax over the token's unmasked logits;  c_e = s_e + bias[e]
+ *   (bias: device fp32 [E_global] of finite values, or NULL for 0; it steers the choice
+ *   and is no part of the weight);
+ *   groups: n_group runs of E_global / n_group consecutive experts, each scored by the sum
+ *   of its group_top (1 or 2) largest c; the topk_group best stay, ties to the lower group;
+ *   topk_ids[t, r] = the kept expert with the r-th largest c, ties to the lower id (without
+ *   a bias the logits themselves are compared, which is the same order and never rounds);
+ *   topk_weights[t, r] = scale * s_e, divided by the sum over the chosen when renormalize
+ *   is not 0 (0 where that sum is 0).
+ * The choice is decided as in exact arithmetic (FP64 wherever FP32 could not tell).
+ * A logit that is NaN, -inf or the lowest finite value of its type masks its expert:
+ * it is never chosen and has no part in the softmax. +inf counts as the largest finite
+ * value. Where fewer than topk experts are left, the remaining slots get id -1 and
+ * weight 0 (the routing sort skips them), so a padded row whose logits are all masked
+ * costs no expert work.
+ * Then the routing tensors of chord_moe_align(topk_ids, T, topk, E, block_m, ...).
+ *
+ * logits: device [T, ld_logits] of logits_dtype (CHORD_DTYPE_*), the first E_global of
+ * each row are read. The other arguments, limits and the workspace rule are those of
+ * chord_moe_align, plus: topk <= E_global <= 1024, 1 <= n_group <= 32, E_global % n_group
+ * == 0, 1 <= topk_group <= n_group, topk <= topk_group * (E_global / n_group), finite scale.
+ * Up to 8 tokens run as one launch.
+ * ---------------------------------------------------------------------------------- */
+CHORD_API chord_status_t chord_router_scored_align(
+    const void* logits, int logits_dtype, int64_t ld_logits, const float* bias, int64_t T, int E_global, int topk,
+    int E, int block_m, int score, int n_group, int topk_group, int group_top, int renormalize, float scale,
+    int32_t* topk_ids, float* topk_weights, int32_t* sorted_ids, int32_t* expert_ids,
+    int32_t* num_tokens_padded /* [2] */, int32_t* expert_offsets /* [E+1] or NULL */, void* workspace,
+    size_t workspace_bytes, chord_stream_t stream);
+
 /* Routing sort for callers that cannot allocate device memory (no counterpart on the
  * pages). Same arguments, results and limits as chord_moe_align, minus the workspace:
  * the scratch that large batches need lives in a static device array of 576 KiB that
@@ -297,6 +341,74 @@ CHORD_API chord_status_t chord_grouped_masked(const uint16_t* x, int E, int64_t 
                                               const int32_t* masked_m, int64_t expected_m, const void* w, int N,
                                               uint16_t* out, void* workspace, size_t workspace_bytes, int flags,
                                               chord_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * FP8 blocks of 128: products of E4M3 activations and weights with one FP32 scale for each
+ * block of 128, for what a model keeps in FP8 around the INT4 experts (its shared expert,
+ * dense layers, or experts held in FP8). No counterpart on the pages, whose layer is W4A16.
+ *
+ * Operands. Activations: codes xq e4m3 [rows, K] row-major, scales xs fp32 [ceil(K/128),
+ * rows] (block-major: one run of `rows` scales for each 128 k). Weights as checkpoints hold
+ * them: codes w e4m3 [E, N, K], scales ws fp32 [E, ceil(N/128), ceil(K/128)]. The last
+ * block of a dimension may be partial.
+ *   out[m, n] = sum over kb of xs[kb, m] * ws[e_m, n/128, kb] * (sum over k in block kb of
+ *               xq[m, k] * w[e_m][n, k])
+ * All sums are FP32 (the inner one in the tensor core, at most 128 exact products); out is
+ * bf16, rounded once, or with CHORD_FLAG_OUTPUT_FP32 the FP32 sums (a tensor-parallel
+ * rank's partial). The result of a row depends on neither the other rows nor the call.
+ *
+ * Requires K % 16 == 0, N % 8 == 0, xq, w and out 16-byte aligned, xs and ws 4-byte
+ * aligned, rows < 2^31 - 256, 1 <= E <= 1024. Every element of out that belongs to a row of
+ * some expert is written, and no other.
+ *
+ * chord_fp8_gemm: one matrix (E = 1), every row. w [N, K], ws [ceil(N/128), ceil(K/128)].
+ * chord_fp8_grouped_contiguous, chord_fp8_grouped_masked: the row layouts, m_indices /
+ *   masked_m / expected_m, the device errors and the unwritten rows of
+ *   chord_grouped_contiguous and chord_grouped_masked.
+ * workspace: device, >= chord_fp8_workspace_bytes(rows, E) bytes (E = 1 for the dense
+ *   product), 256-byte aligned; its first CHORD_WORKSPACE_HEADER_BYTES hold the status word
+ *   (zero once; read with chord_moe_check_status), the rest is scratch. Calls that overlap
+ *   on the GPU must not share it.
+ * flags: CHORD_FLAG_OUTPUT_FP32; CHORD_FLAG_FORCE_STREAM / CHORD_FLAG_FORCE_TENSOR pick
+ *   the schedule (by default from the rows, or rows per expert). The schedules differ in
+ *   the order of the FP32 sums.
+ *
+ * chord_fp8_quantize: activations to E4M3 in blocks of 128 along K, per row r and block b:
+ *   amax = max(max |x|, 2^-100); scales[b, r] = amax / 448; q = e4m3_rne(x * (448 / amax)),
+ *   each operation rounded to FP32. A block that holds an infinity or a NaN gets scale NaN.
+ *   x: device [rows, ldx] of x_dtype (CHORD_DTYPE_F32 or _BF16), the first K of each row
+ *   are read; 16-byte aligned rows (x and ldx * element size). masked_m (device int32 [E], or NULL with E = 0):
+ *   rows = E * max_m in the masked layout; rows m with m % max_m >= masked_m[m / max_m] are
+ *   neither read nor written (counts are clamped to [0, max_m]).
+ * chord_fp8_silu_quantize: the same of silu(h[r, 0:I]) * h[r, I:2I], computed in FP32; h:
+ *   [rows, ldh] of h_dtype, ldh >= 2I. I % 16 == 0.
+ * chord_fp8_gate_up: h = chord_fp8_gemm with w13 [2I, H] (gate rows first) kept in FP32,
+ *   then chord_fp8_silu_quantize of it: q e4m3 [M, I] and scales [I/128, M], the operands
+ *   of the down product. I % 128 == 0. workspace: >= chord_fp8_gate_up_workspace_bytes(M, I)
+ *   bytes, rules as above.
+ * ---------------------------------------------------------------------------------- */
+CHORD_API size_t chord_fp8_workspace_bytes(int64_t rows, int E);
+CHORD_API chord_status_t chord_fp8_quantize(const void* x, int x_dtype, int64_t ldx, int64_t rows, int K,
+                                            const int32_t* masked_m, int E, uint8_t* q, float* scales,
+                                            chord_stream_t stream);
+CHORD_API chord_status_t chord_fp8_silu_quantize(const void* h, int h_dtype, int64_t ldh, int64_t rows, int I,
+                                                 const int32_t* masked_m, int E, uint8_t* q, float* scales,
+                                                 chord_stream_t stream);
+CHORD_API chord_status_t chord_fp8_gemm(const uint8_t* xq, const float* xs, int64_t M, int K, const uint8_t* w,
+                                        const float* ws, int N, void* out, void* workspace, size_t workspace_bytes,
+                                        int flags, chord_stream_t stream);
+CHORD_API chord_status_t chord_fp8_grouped_contiguous(const uint8_t* xq, const float* xs, int64_t M, int K,
+                                                      const int32_t* m_indices, const uint8_t* w, const float* ws,
+                                                      int E, int N, void* out, void* workspace,
+                                                      size_t workspace_bytes, int flags, chord_stream_t stream);
+CHORD_API chord_status_t chord_fp8_grouped_masked(const uint8_t* xq, const float* xs, int E, int64_t max_m, int K,
+                                                  const int32_t* masked_m, int64_t expected_m, const uint8_t* w,
+                                                  const float* ws, int N, void* out, void* workspace,
+                                                  size_t workspace_bytes, int flags, chord_stream_t stream);
+CHORD_API size_t chord_fp8_gate_up_workspace_bytes(int64_t M, int I);
+CHORD_API chord_status_t chord_fp8_gate_up(const uint8_t* xq, const float* xs, int64_t M, int H, const uint8_t* w13,
+                                           const float* ws13, int I, uint8_t* q, float* scales, void* workspace,
+                                           size_t workspace_bytes, int flags, chord_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * Exchange steps of sharded deployments. The Chord blog runs the layer as expert-parallel

@@ -43,6 +43,15 @@ CHORD_FLAG_FORCE_STREAM = 0x2
 CHORD_FLAG_FORCE_TENSOR = 0x4
 CHORD_FLAG_OUTPUT_FP32 = 0x8
 
+CHORD_DTYPE_F32 = 0
+CHORD_DTYPE_BF16 = 1
+CHORD_DTYPE_F16 = 2
+_DTYPES = {torch.float32: CHORD_DTYPE_F32, torch.bfloat16: CHORD_DTYPE_BF16, torch.float16: CHORD_DTYPE_F16}
+
+CHORD_SCORE_SOFTMAX = 0
+CHORD_SCORE_SIGMOID = 1
+_SCORES = {"softmax": CHORD_SCORE_SOFTMAX, "sigmoid": CHORD_SCORE_SIGMOID}
+
 # every symbol include/chord.h declares: (name, restype, argtypes)
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -65,9 +74,19 @@ SIGNATURES = {
     "chord_moe_check_status": (_I, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "chord_moe_align_noalloc": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _P, _P]),
     "chord_router_topk_align": (_I, [_P, _I64, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "chord_router_scored_align": (_I, [_P, _I, _I64, _P, _I64, _I, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P,
+                                       _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "chord_grouped_workspace_bytes": (_SZ, [_I64, _I]),
     "chord_grouped_contiguous": (_I, [_P, _I64, _I, _P, _P, _I, _I, _P, _P, _SZ, _I, _P]),
     "chord_grouped_masked": (_I, [_P, _I, _I64, _I, _P, _I64, _P, _I, _P, _P, _SZ, _I, _P]),
+    "chord_fp8_workspace_bytes": (_SZ, [_I64, _I]),
+    "chord_fp8_quantize": (_I, [_P, _I, _I64, _I64, _I, _P, _I, _P, _P, _P]),
+    "chord_fp8_silu_quantize": (_I, [_P, _I, _I64, _I64, _I, _P, _I, _P, _P, _P]),
+    "chord_fp8_gemm": (_I, [_P, _P, _I64, _I, _P, _P, _I, _P, _P, _SZ, _I, _P]),
+    "chord_fp8_grouped_contiguous": (_I, [_P, _P, _I64, _I, _P, _P, _P, _I, _I, _P, _P, _SZ, _I, _P]),
+    "chord_fp8_grouped_masked": (_I, [_P, _P, _I, _I64, _I, _P, _I64, _P, _P, _I, _P, _P, _SZ, _I, _P]),
+    "chord_fp8_gate_up_workspace_bytes": (_SZ, [_I64, _I]),
+    "chord_fp8_gate_up": (_I, [_P, _P, _I64, _I, _P, _P, _I, _P, _P, _P, _SZ, _I, _P]),
     "chord_ep_plan_workspace_bytes": (_SZ, [_I64, _I]),
     "chord_ep_plan": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "chord_ep_pack": (_I, [_P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
@@ -114,6 +133,26 @@ def _ptr(t):
         return None
     assert t.is_cuda and t.is_contiguous(), "device tensors must be contiguous CUDA tensors"
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows_ptr(t):
+    """Pointer of a 2-D tensor whose rows are contiguous but may lie apart (a slice of wider
+    rows), and the distance between rows in elements."""
+    assert t.is_cuda and t.dim() == 2, "expected a 2-D CUDA tensor"
+    if t.shape[0] <= 1 or t.shape[1] == 0:
+        ld = t.shape[1]
+    else:
+        ld = t.stride(0)
+    assert t.shape[1] <= 1 or t.stride(1) == 1, "rows must be contiguous"
+    assert ld >= t.shape[1], "rows must not overlap"
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def _typed(t, dtype, what, numel=None):
+    """`t` (or None) after a check of its type and, if given, its number of elements."""
+    assert t is None or t.dtype == dtype, f"{what} must be {dtype}, not {t.dtype}"
+    assert t is None or numel is None or t.numel() >= numel, f"{what} holds {t.numel()} elements, needs {numel}"
+    return t
 
 
 def _stream(stream=None):
@@ -199,6 +238,33 @@ def chord_router_topk_align(logits, topk, E, block_m, topk_ids, topk_weights, so
                                          ws_bytes, _stream(stream)), "chord_router_topk_align")
 
 
+def chord_router_scored_align(logits, topk, E, block_m, topk_ids, topk_weights, sorted_ids, expert_ids,
+                              num_tokens_padded, expert_offsets=None, workspace=None, *, bias=None, score="sigmoid",
+                              n_group=1, topk_group=1, group_top=1, renormalize=True, scale=1.0, stream=None):
+    """Router with softmax or sigmoid scores, a bias on the choice, expert groups and scaled
+    weights, fused with the routing sort over the local experts [0, E). logits: fp32, bf16
+    or fp16 [T, E_global], rows may lie apart."""
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', not {score!r}")
+    assert logits.dtype in _DTYPES, f"logits must be fp32, bf16 or fp16, not {logits.dtype}"
+    T, G = logits.shape
+    ptr, ld = _rows_ptr(logits)
+    _typed(topk_ids, torch.int32, "topk_ids", T * topk)
+    _typed(topk_weights, torch.float32, "topk_weights", T * topk)
+    _typed(bias, torch.float32, "bias", G)
+    cap = chord_moe_align_capacity(T, topk, E, block_m)
+    _typed(sorted_ids, torch.int32, "sorted_ids", cap)
+    _typed(expert_ids, torch.int32, "expert_ids", (cap + block_m - 1) // block_m if block_m > 0 else None)
+    _typed(expert_offsets, torch.int32, "expert_offsets", E + 1)
+    ws_bytes = 0 if workspace is None else _nbytes(workspace)
+    _check(lib().chord_router_scored_align(ptr, _DTYPES[logits.dtype], ld, _ptr(bias), T, G, topk, E, block_m,
+                                           _SCORES[score], n_group, topk_group, group_top, int(bool(renormalize)),
+                                           float(scale), _ptr(topk_ids), _ptr(topk_weights), _ptr(sorted_ids),
+                                           _ptr(expert_ids), _ptr(_routing_header(num_tokens_padded)),
+                                           _ptr(expert_offsets), _ptr(workspace), ws_bytes, _stream(stream)),
+           "chord_router_scored_align")
+
+
 def chord_repack_weights(qweight, scales, role, out, group_size=32, stream=None):
     E, N, K8 = qweight.shape
     _check(lib().chord_repack_weights(_ptr(qweight), _ptr(scales), E, N, K8 * 8, group_size, role,
@@ -240,6 +306,112 @@ def chord_grouped_masked(x, masked_m, expected_m, w, N, out, workspace, flags=0,
     _check(lib().chord_grouped_masked(_ptr(x), E, max_m, K, _ptr(masked_m), int(expected_m), _ptr(w), N,
                                       _ptr(out), _ptr(workspace), _nbytes(workspace), flags, _stream(stream)),
            "chord_grouped_masked")
+
+
+# FP8 in blocks of 128: codes e4m3 [rows, K] with scales fp32 [ceil(K/128), rows]; weights
+# e4m3 [E, N, K] (or [N, K]) with scales fp32 [E, ceil(N/128), ceil(K/128)].
+
+def _fp8_codes(t, what, shape=None):
+    assert t.dtype in (torch.float8_e4m3fn, torch.uint8), f"{what} must hold e4m3 codes, not {t.dtype}"
+    assert shape is None or tuple(t.shape) == tuple(shape), f"{what} has shape {tuple(t.shape)}, needs {tuple(shape)}"
+    return _ptr(t)
+
+
+def _fp8_scales(t, what, shape):
+    _typed(t, torch.float32, what)
+    assert tuple(t.shape) == tuple(shape), f"{what} has shape {tuple(t.shape)}, needs {tuple(shape)}"
+    return _ptr(t)
+
+
+def _fp8_out(out, rows, N, flags):
+    assert tuple(out.shape) == (rows, N), f"out has shape {tuple(out.shape)}, needs {(rows, N)}"
+    assert out.dtype in (torch.bfloat16, torch.float32), f"out must be bf16 or fp32, not {out.dtype}"
+    return _ptr(out), flags | (CHORD_FLAG_OUTPUT_FP32 if out.dtype == torch.float32 else 0)
+
+
+def _blocks128(n) -> int:
+    return (n + 127) // 128
+
+
+def chord_fp8_workspace_bytes(rows, E=1) -> int:
+    return int(lib().chord_fp8_workspace_bytes(rows, E))
+
+
+def chord_fp8_gate_up_workspace_bytes(M, I) -> int:
+    return int(lib().chord_fp8_gate_up_workspace_bytes(M, I))
+
+
+def _fp8_quantize(name, x, q, scales, masked_m, width, stream):
+    x2 = x.flatten(0, 1) if x.dim() == 3 else x  # [E, max_m, K] of the masked layout
+    q2 = q.flatten(0, 1) if q.dim() == 3 else q
+    rows, K = q2.shape
+    assert tuple(x2.shape) == (rows, width * K), f"input has shape {tuple(x2.shape)}, codes {tuple(q2.shape)}"
+    assert x.dtype in (torch.bfloat16, torch.float32), f"input must be bf16 or fp32, not {x.dtype}"
+    ptr, ld = _rows_ptr(x2)
+    _typed(masked_m, torch.int32, "masked_m")
+    _check(getattr(lib(), name)(ptr, _DTYPES[x.dtype], ld, rows, K, _ptr(masked_m),
+                                0 if masked_m is None else masked_m.numel(), _fp8_codes(q2, "q"),
+                                _fp8_scales(scales, "scales", (_blocks128(K), rows)), _stream(stream)), name)
+
+
+def chord_fp8_quantize(x, q, scales, masked_m=None, stream=None):
+    """q (e4m3 [rows, K]) and scales (fp32 [ceil(K/128), rows]) of bf16 or fp32 rows x."""
+    _fp8_quantize("chord_fp8_quantize", x, q, scales, masked_m, 1, stream)
+
+
+def chord_fp8_silu_quantize(h, q, scales, masked_m=None, stream=None):
+    """q and scales of silu(h[:, :I]) * h[:, I:], bf16 or fp32 rows h [rows, 2 I]."""
+    _fp8_quantize("chord_fp8_silu_quantize", h, q, scales, masked_m, 2, stream)
+
+
+def chord_fp8_gemm(xq, xs, w, ws, out, workspace, flags=0, stream=None):
+    """out [M, N] (bf16, or fp32 sums if out is fp32) = dequantised xq [M, K] times w [N, K]^T."""
+    M, K = xq.shape
+    N = w.shape[0]
+    po, flags = _fp8_out(out, M, N, flags)
+    _check(lib().chord_fp8_gemm(_fp8_codes(xq, "xq"), _fp8_scales(xs, "xs", (_blocks128(K), M)), M, K,
+                                _fp8_codes(w, "w", (N, K)), _fp8_scales(ws, "ws", (_blocks128(N), _blocks128(K))), N,
+                                po, _ptr(workspace), _nbytes(workspace), flags, _stream(stream)), "chord_fp8_gemm")
+
+
+def chord_fp8_grouped_contiguous(xq, xs, m_indices, w, ws, out, workspace, flags=0, stream=None):
+    """The grouped product over rows concatenated by expert (layout of chord_grouped_contiguous)."""
+    M, K = xq.shape
+    E, N, _ = w.shape
+    po, flags = _fp8_out(out, M, N, flags)
+    _typed(m_indices, torch.int32, "m_indices", M)
+    _check(lib().chord_fp8_grouped_contiguous(
+        _fp8_codes(xq, "xq"), _fp8_scales(xs, "xs", (_blocks128(K), M)), M, K, _ptr(m_indices),
+        _fp8_codes(w, "w", (E, N, K)), _fp8_scales(ws, "ws", (E, _blocks128(N), _blocks128(K))), E, N, po,
+        _ptr(workspace), _nbytes(workspace), flags, _stream(stream)), "chord_fp8_grouped_contiguous")
+
+
+def chord_fp8_grouped_masked(xq, xs, masked_m, expected_m, w, ws, out, workspace, flags=0, stream=None):
+    """The grouped product over a fixed row budget per expert (layout of chord_grouped_masked);
+    xq is [E, max_m, K] or [E * max_m, K], out [E * max_m, N]."""
+    E, N, K = w.shape
+    x2 = xq.flatten(0, 1) if xq.dim() == 3 else xq
+    rows = x2.shape[0]
+    assert masked_m.numel() == E and rows % E == 0, f"{rows} rows and {masked_m.numel()} counts for {E} experts"
+    po, flags = _fp8_out(out, rows, N, flags)
+    _typed(masked_m, torch.int32, "masked_m")
+    _check(lib().chord_fp8_grouped_masked(
+        _fp8_codes(x2, "xq", (rows, K)), _fp8_scales(xs, "xs", (_blocks128(K), rows)), E, rows // E, K,
+        _ptr(masked_m), int(expected_m), _fp8_codes(w, "w"),
+        _fp8_scales(ws, "ws", (E, _blocks128(N), _blocks128(K))), N, po, _ptr(workspace), _nbytes(workspace), flags,
+        _stream(stream)), "chord_fp8_grouped_masked")
+
+
+def chord_fp8_gate_up(xq, xs, w13, ws13, q, scales, workspace, flags=0, stream=None):
+    """q (e4m3 [M, I]) and scales of silu(gate) * up, [gate | up] = dequantised xq [M, H] times
+    w13 [2 I, H]^T."""
+    M, H = xq.shape
+    I2 = w13.shape[0]
+    _check(lib().chord_fp8_gate_up(
+        _fp8_codes(xq, "xq"), _fp8_scales(xs, "xs", (_blocks128(H), M)), M, H, _fp8_codes(w13, "w13", (I2, H)),
+        _fp8_scales(ws13, "ws13", (_blocks128(I2), _blocks128(H))), I2 // 2, _fp8_codes(q, "q", (M, I2 // 2)),
+        _fp8_scales(scales, "scales", (_blocks128(I2 // 2), M)), _ptr(workspace), _nbytes(workspace), flags,
+        _stream(stream)), "chord_fp8_gate_up")
 
 
 def chord_ep_plan_workspace_bytes(T, W) -> int:
@@ -368,15 +540,90 @@ class ChordMoE:
         chord_moe_align(topk_ids, self.E, self.block_m, self.sorted_ids, self.expert_ids, self.ntp,
                         self.offsets, self.align_ws)
 
+    def route(self, logits, topk_ids=None, topk_weights=None, **scoring):
+        """Routes by gate logits [T, E_global] and sorts for this layer's buffers; `scoring` are
+        the keyword arguments of chord_router_scored_align (bias, score, n_group, topk_group,
+        group_top, renormalize, scale). Returns (topk_ids, topk_weights)."""
+        T = logits.shape[0]
+        if T > self.max_tokens:
+            self.reserve(T)
+        if topk_ids is None:
+            topk_ids = torch.empty((T, self.topk), dtype=torch.int32, device=self.device)
+        if topk_weights is None:
+            topk_weights = torch.empty((T, self.topk), dtype=torch.float32, device=self.device)
+        chord_router_scored_align(logits, self.topk, self.E, self.block_m, topk_ids, topk_weights, self.sorted_ids,
+                                  self.expert_ids, self.ntp, self.offsets, self.align_ws, **scoring)
+        return topk_ids, topk_weights
+
+    def forward_logits(self, hidden, logits, out=None, flags=0, **scoring):
+        """The layer from gate logits: route() and forward in one. Returns (out, topk_ids,
+        topk_weights)."""
+        topk_ids, topk_weights = self.route(logits, **scoring)
+        return self._forward_sorted(hidden, topk_ids, topk_weights, out, flags), topk_ids, topk_weights
+
     def forward(self, hidden, topk_ids, topk_weights, out=None, flags=0):
         T = hidden.shape[0]
         if T > self.max_tokens:
             self.reserve(T)
-        if out is None:
-            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         self.align(topk_ids)
+        return self._forward_sorted(hidden, topk_ids, topk_weights, out, flags)
+
+    def _forward_sorted(self, hidden, topk_ids, topk_weights, out, flags):
+        if out is None:
+            out = torch.empty((hidden.shape[0], self.H), dtype=torch.bfloat16, device=self.device)
         chord_moe_forward(hidden, topk_ids, topk_weights, self.sorted_ids, self.expert_ids, self.ntp,
                           self.block_m, self.w13, self.w2, self.I, self.E, out, self.workspace, flags)
+        return out
+
+    __call__ = forward
+
+    def check_status(self) -> int:
+        return chord_moe_check_status(self.workspace)
+
+
+class ChordFP8MLP:
+    """A gated MLP held in FP8 blocks of 128, such as the shared expert next to a ChordMoE:
+    y = W2 . (silu(gate) * up), [gate | up] = W13 . x, activations quantised per row and
+    block on the way.
+
+    w13 e4m3 [2 I, H] (gate rows first) with scales fp32 [2 I/128, H/128], w2 e4m3 [H, I] with
+    scales [H/128, I/128]; the tensors are kept as they are. Buffers are sized for up to
+    ``max_tokens`` tokens; call with any T <= max_tokens.
+    """
+
+    def __init__(self, w13, s13, w2, s2, max_tokens=1):
+        self.w13, self.s13, self.w2, self.s2 = w13, s13, w2, s2
+        self.H, self.I = w13.shape[1], w13.shape[0] // 2
+        if tuple(w2.shape) != (self.H, self.I):
+            raise ValueError(f"w2 has shape {tuple(w2.shape)}, w13 {tuple(w13.shape)}")
+        self.device = w13.device
+        self.max_tokens = -1
+        self.reserve(max_tokens)
+
+    def reserve(self, T: int):
+        d = self.device
+        self.xq = _alloc_bytes(T * self.H, d)
+        self.xs = torch.empty(max(T * _blocks128(self.H), 1), dtype=torch.float32, device=d)
+        self.aq = _alloc_bytes(T * self.I, d)
+        self.as_ = torch.empty(max(T * _blocks128(self.I), 1), dtype=torch.float32, device=d)
+        need = max(chord_fp8_gate_up_workspace_bytes(T, self.I), chord_fp8_workspace_bytes(T, 1))
+        self.workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=d)
+        self.max_tokens = T
+
+    def forward(self, x, out=None, flags=0):
+        """out [T, H] (bf16, or the fp32 sums if an fp32 `out` is given) for bf16 or fp32 x [T, H]."""
+        T = x.shape[0]
+        if T > self.max_tokens:
+            self.reserve(T)
+        if out is None:
+            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+        if T == 0:
+            return out
+        xq, xs = self.xq[:T * self.H].view(T, self.H), self.xs[:T * _blocks128(self.H)].view(-1, T)
+        aq, a_s = self.aq[:T * self.I].view(T, self.I), self.as_[:T * _blocks128(self.I)].view(-1, T)
+        chord_fp8_quantize(x, xq, xs)
+        chord_fp8_gate_up(xq, xs, self.w13, self.s13, aq, a_s, self.workspace, flags)
+        chord_fp8_gemm(aq, a_s, self.w2, self.s2, out, self.workspace, flags)
         return out
 
     __call__ = forward

@@ -1,5 +1,7 @@
 // api.cu -- the C ABI declared in include/chord.h: argument checks, the prepared-weight
 // registry, the memoised schedule selector and the launch sequence of the layer.
+#include <math.h>
+
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -178,6 +180,64 @@ chord_status_t chord_router_topk_align(const float* logits, int64_t T, int E_glo
                                         workspace, reinterpret_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "router + moe_align launch");
   return CHORD_OK;
+}
+
+chord_status_t chord_router_scored_align(const void* logits, int logits_dtype, int64_t ld_logits, const float* bias,
+                                         int64_t T, int E_global, int topk, int E, int block_m, int score,
+                                         int n_group, int topk_group, int group_top, int renormalize, float scale,
+                                         int32_t* topk_ids, float* topk_weights, int32_t* sorted_ids,
+                                         int32_t* expert_ids, int32_t* num_tokens_padded, int32_t* expert_offsets,
+                                         void* workspace, size_t workspace_bytes, chord_stream_t stream) {
+  clear_detail();
+  chord_status_t st = check_align_args(T, topk, E, block_m);
+  if (st != CHORD_OK) return st;
+  if (E_global < topk || E_global > 1024)
+    return fail(CHORD_ERR_UNSUPPORTED, "E_global=%d outside [topk=%d, 1024]", E_global, topk);
+  if (logits_dtype < CHORD_DTYPE_F32 || logits_dtype > CHORD_DTYPE_F16)
+    return fail(CHORD_ERR_UNSUPPORTED, "logits_dtype=%d", logits_dtype);
+  if (score != CHORD_SCORE_SOFTMAX && score != CHORD_SCORE_SIGMOID)
+    return fail(CHORD_ERR_UNSUPPORTED, "score=%d", score);
+  if (n_group < 1 || n_group > 32 || E_global % n_group)
+    return fail(CHORD_ERR_UNSUPPORTED, "n_group=%d must be in [1, 32] and divide E_global=%d", n_group, E_global);
+  if (topk_group < 1 || topk_group > n_group || group_top < 1 || group_top > 2)
+    return fail(CHORD_ERR_INVALID_ARG, "topk_group=%d of n_group=%d, group_top=%d", topk_group, n_group, group_top);
+  if (topk > topk_group * (E_global / n_group))
+    return fail(CHORD_ERR_INVALID_ARG, "topk=%d experts out of %d groups of %d", topk, topk_group, E_global / n_group);
+  if (!(scale > -INFINITY && scale < INFINITY)) return fail(CHORD_ERR_INVALID_ARG, "scale is not finite");
+  if (ld_logits < E_global)
+    return fail(CHORD_ERR_INVALID_ARG, "ld_logits=%lld below E_global=%d", (long long)ld_logits, E_global);
+  if ((T > 0 && (!logits || !topk_ids || !topk_weights)) || !sorted_ids || !expert_ids || !num_tokens_padded)
+    return fail(CHORD_ERR_INVALID_ARG, "null routing pointer");
+  const size_t need = align_workspace_bytes(T * topk, E);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(CHORD_ERR_WORKSPACE_TOO_SMALL, "align workspace needs %zu bytes, got %zu", need,
+                workspace ? workspace_bytes : size_t(0));
+  if (need > 0 && !aligned256(workspace)) return fail(CHORD_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  int num_sms = 0;
+  if ((st = current_device(&num_sms)) != CHORD_OK) return st;
+  RouterArgs p{};
+  p.logits = logits;
+  p.bias = bias;
+  p.topk_ids = topk_ids;
+  p.topk_weights = topk_weights;
+  p.T = T;
+  p.ld = ld_logits;
+  p.dtype = logits_dtype;
+  p.G = E_global;
+  p.k = topk;
+  p.score = score;
+  p.n_group = n_group;
+  p.group_size = E_global / n_group;
+  p.group_magic = ((uint64_t(1) << 32) + p.group_size - 1) / p.group_size;
+  p.topk_group = topk_group;
+  p.group_top = group_top;
+  p.renormalize = renormalize != 0;
+  p.scale = scale;
+  const cudaError_t err = launch_router_scored(
+      p, E, block_m, chord_moe_align_capacity(T, topk, E, block_m), chord_moe_align_num_blocks(T, topk, E, block_m),
+      sorted_ids, expert_ids, num_tokens_padded, expert_offsets, workspace, num_sms,
+      reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? CHORD_OK : cuda_fail(err, "scored router + moe_align launch");
 }
 
 size_t chord_repacked_bytes(int E, int N, int K, int group_size) {

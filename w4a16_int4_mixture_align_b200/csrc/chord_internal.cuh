@@ -393,6 +393,20 @@ cudaError_t launch_router_align(const float* logits, int64_t T, int G, int k, in
                                 int32_t* sorted_ids, int32_t* expert_ids, int32_t* ntp, int32_t* offsets,
                                 void* workspace, cudaStream_t stream);
 size_t align_workspace_bytes(int64_t n, int E);
+// Scored router then the routing sort (router.cu).
+struct RouterArgs {
+  const void* logits;  // [T, ld] of `dtype` (CHORD_DTYPE_*), the first G of each row
+  const float* bias;   // [G] or null
+  int32_t* topk_ids;   // [T, k]
+  float* topk_weights;
+  int64_t T, ld;
+  uint64_t group_magic;  // ceil(2^32 / group_size): e / group_size = e * magic >> 32 for e < 1024
+  int dtype, G, k, score, n_group, group_size, topk_group, group_top, renormalize;
+  float scale;
+};
+cudaError_t launch_router_scored(const RouterArgs& p, int E, int block_m, int64_t cap, int64_t nblocks,
+                                 int32_t* sorted_ids, int32_t* expert_ids, int32_t* ntp, int32_t* offsets,
+                                 void* workspace, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_repack(const int32_t* qweight, const uint16_t* scales, int E, int N, int K,
                           int role, uint8_t* blob, cudaStream_t stream);

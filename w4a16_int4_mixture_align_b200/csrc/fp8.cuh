@@ -1,0 +1,58 @@
+// fp8.cuh -- what the FP8 block-128 kernels and their entry points share.
+#pragma once
+
+#include "chord_internal.cuh"
+
+namespace chord {
+
+constexpr int kFp8Block = 128;  // elements under one scale
+constexpr float kFp8Max = 448.f;
+
+__host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// Workspace of the products: the zero-once header, then the unit lists of the grouped
+// layouts (units of 8 to 256 rows, written by the routing pass).
+struct Fp8Workspace {
+  int64_t max_positions, ntp_offset, expert_ids_offset, block_row0_offset, sorted_ids_offset, total;
+};
+Fp8Workspace fp8_workspace(int64_t rows, int E);
+
+enum Fp8Layout { kFp8Dense = 0, kFp8Contiguous = 1, kFp8Masked = 2 };
+
+struct Fp8Args {
+  const uint8_t* xq;  // e4m3 [rows, K]
+  const float* xs;    // [fp8_blocks(K), rows]
+  const uint8_t* w;   // e4m3 [E, N, K]
+  const float* ws;    // [E, fp8_blocks(N), fp8_blocks(K)]
+  void* out;          // [rows, N] bf16, or FP32 if out_f32
+  int64_t rows;
+  int K, N, E, layout;
+  int out_f32;
+  // grouped layouts: units of bm rows (the routing pass's lists); dense: null
+  const int32_t* sorted_ids;  // row of each position, -1 where it belongs to no expert
+  const int32_t* expert_ids;  // expert of each unit
+  const int32_t* block_row0;  // row of each unit's first position
+  const int32_t* ntp;         // units * bm
+  int bm;
+  uint32_t* status;
+  int num_sms;
+};
+
+struct Fp8QuantArgs {
+  const void* x;
+  int dtype;  // CHORD_DTYPE_F32 or CHORD_DTYPE_BF16
+  int64_t ld, rows;
+  int K;      // columns of the codes
+  int silu;   // x holds [gate | up], 2K columns
+  const int32_t* masked_m;  // or null
+  int64_t max_m;
+  uint8_t* q;
+  float* scales;
+  int num_sms;
+};
+
+cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t stream);
+// Any number of rows; a.bm in {8, 16, 32}.
+cudaError_t launch_fp8_stream(const Fp8Args& a, cudaStream_t stream);
+
+}  // namespace chord

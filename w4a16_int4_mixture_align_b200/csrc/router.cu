@@ -1,0 +1,458 @@
+// router.cu -- scored routing to experts: softmax or sigmoid scores, a balance bias on the
+// choice, expert groups, top-k, renormalised and scaled weights.
+//
+// Per token, with logits l_e, bias b_e (optional) and G experts in n_group equal runs:
+//   s_e = sigmoid(l_e), or softmax over the token's unmasked logits;
+//   c_e = s_e + b_e               what experts are chosen by (a masked expert never is);
+//   group score = sum of the group_top (1 or 2) largest c of the group; the topk_group
+//   best groups stay; then the topk largest c among them, in descending order;
+//   w = s_e of the chosen (without the bias), over their sum if renormalised, x scale.
+// A logit that is NaN, -inf or the lowest value of its type masks its expert.
+//
+// The choice is that of exact arithmetic, ties going to the lower id, although almost all
+// of the work is in FP32: two experts whose c differ by less than FP32 resolves would
+// otherwise be ordered by rounding. One warp owns a token:
+//   1. c in FP32 for every expert (lane l: experts l, l + 32, ...). Without a bias both
+//      scores grow with the logit, so the logit itself is the key and nothing rounds.
+//   2. the k-th largest of the 32 lane maxima is at most the k-th largest c, so every
+//      expert of the answer is among those with c >= that threshold minus the FP32 error
+//      bound. Typically 8 to 12 of 384 experts are; they are compacted to one per lane.
+//   3. one c in FP64 per lane, the rank of each by counting larger ones, and the weights.
+// Groups are scored in FP32 as well; a border between a kept and a dropped group closer
+// than the error bound, more than 32 candidates, or k > 32 take the slow way: every c in
+// FP64 in shared memory, then k rounds of a warp-wide maximum.
+//
+// Bound: reading the logits (T=8192, G=384, FP32: 12.6 MB) and, below that, issue slots:
+// about 30 instructions per expert slot of a lane.
+#include <math.h>
+
+#include "align_common.cuh"
+
+namespace chord {
+namespace {
+
+constexpr int kRouterWarps = 8;
+constexpr unsigned kFull = 0xffffffffu;
+// |c in FP32 - c| <= 1e-6 + |c| * 2^-24 for both scores (a sum of G exponentials and one
+// division, each exponential within a few ulp); thresholds stay four times further away.
+constexpr float kSlackAbs = 4e-6f, kSlackRel = 1e-6f;
+
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((b & 0x80000000u) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ float warp_max(float v) { return order_value(__reduce_max_sync(kFull, order_key(v))); }
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// The logit as FP32, -inf where it masks its expert, +inf as the largest finite value.
+__device__ __forceinline__ float load_logit(const RouterArgs& p, int64_t row, int e) {
+  if (p.dtype == CHORD_DTYPE_F32) {
+    const float v = __ldg(static_cast<const float*>(p.logits) + row + e);
+    return v > -3.402823466e38f ? fminf(v, 3.402823466e38f) : -INFINITY;
+  }
+  if (p.dtype == CHORD_DTYPE_BF16) {
+    const float v = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p.logits) + row + e)) << 16);
+    return v > -3.38953139e38f ? fminf(v, 3.38953139e38f) : -INFINITY;
+  }
+  const float v = __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t*>(p.logits) + row + e)));
+  return v > -65504.f ? fminf(v, 65504.f) : -INFINITY;
+}
+
+// s in FP64. `lmax` and `z` (the softmax denominator) are unused for sigmoid.
+__device__ __forceinline__ double score64(const RouterArgs& p, float l, float lmax, double z) {
+  if (p.score == CHORD_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-double(l)));
+  return exp(double(l) - double(lmax)) / z;
+}
+
+// The softmax denominator of token t in FP64 (1 if every logit is masked).
+__device__ __noinline__ double softmax_sum64(const RouterArgs& p, int64_t t, float lmax) {
+  double z = 0.0;
+  for (int e = threadIdx.x & 31; e < p.G; e += 32) {
+    const float l = load_logit(p, t * p.ld, e);
+    if (l > -INFINITY) z += exp(double(l) - double(lmax));
+  }
+  z = warp_sum(z);
+  return z > 0.0 ? z : 1.0;
+}
+
+// The kept groups of the token as a bit mask, from the keys v[0..G) in shared memory
+// (-inf: masked). `near` reports a border that the keys' error could move. A team of
+// 32 / (n_group rounded up to a power of two) lanes scans each group.
+template <typename V>
+__device__ __forceinline__ uint32_t kept_groups(const RouterArgs& p, const V* v, float lmax, double slack_abs,
+                                                double slack_rel, bool* near) {
+  const int lane = threadIdx.x & 31;
+  int teams = 1;
+  while (teams < p.n_group) teams <<= 1;
+  const int width = 32 / teams;
+  const int g = lane / width, sub = lane % width;
+  V a1 = V(-INFINITY), a2 = V(-INFINITY);
+  if (g < p.n_group)
+    for (int j = sub; j < p.group_size; j += width) {
+      const V x = v[g * p.group_size + j];
+      if (x > a1) {
+        a2 = a1;
+        a1 = x;
+      } else if (x > a2) {
+        a2 = x;
+      }
+    }
+  for (int o = 1; o < width; o <<= 1) {
+    const V b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+    const V lo = a1 < b1 ? a1 : b1;
+    a1 = a1 < b1 ? b1 : a1;
+    a2 = a2 < b2 ? b2 : a2;
+    a2 = a2 < lo ? lo : a2;
+  }
+  double score = double(a1);
+  if (p.group_top == 2 && a1 > V(-INFINITY)) {
+    // without a bias the keys are logits: their scores add up, not they themselves (the
+    // softmax denominator is common to all groups and left out)
+    const bool two = a2 > V(-INFINITY);
+    if (p.bias) score += two ? double(a2) : 0.0;
+    else score = score64(p, float(a1), lmax, 1.0) + (two ? score64(p, float(a2), lmax, 1.0) : 0.0);
+  }
+  const double size = fabs(double(a1)) + (p.group_top == 2 && a2 > V(-INFINITY) ? fabs(double(a2)) : 0.0);
+  const double off = slack_abs + slack_rel * (a1 > V(-INFINITY) ? size : 0.0);
+  // lane i < n_group takes group i's score; rank by counting
+  const double mine = __shfl_sync(kFull, score, (lane * width) & 31);
+  const double mine_off = __shfl_sync(kFull, off, (lane * width) & 31);
+  int rank = 0;
+  for (int i = 0; i < p.n_group; ++i) {
+    const double o = __shfl_sync(kFull, mine, i);
+    rank += (o > mine || (o == mine && i < lane)) ? 1 : 0;
+  }
+  const bool real = lane < p.n_group && mine > -INFINITY;
+  const uint32_t kept = __ballot_sync(kFull, real && rank < p.topk_group);
+  // in doubt where the least a kept group may have is no more than a dropped one may have
+  const bool in = (kept >> lane) & 1u;
+  double low = in ? mine - mine_off : INFINITY, high = real && !in ? mine + mine_off : -INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    low = fmin(low, __shfl_xor_sync(kFull, low, o));
+    high = fmax(high, __shfl_xor_sync(kFull, high, o));
+  }
+  *near = high >= low;
+  return kept;
+}
+
+// Ranks this lane's candidate (lane < n; c descending, ties to the lower lane). *gap: the
+// smallest distance to another candidate that is not the same number for certain.
+__device__ __forceinline__ int rank_of(double c, int n, double* gap) {
+  const int lane = threadIdx.x & 31;
+  int rank = 0;
+  double d = INFINITY;
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(kFull, c, j);
+    rank += (o > c || (o == c && j < lane)) ? 1 : 0;
+    if (j != lane && lane < n) d = fmin(d, fabs(o - c));
+  }
+  *gap = d;
+  return rank;
+}
+
+// Writes rank `rank`'s id and weight (lanes with `mine`), and empty slots from rank n on.
+__device__ __forceinline__ void write_token(const RouterArgs& p, int64_t t, bool mine, int rank, int e, float l,
+                                            float lmax, double z, int n) {
+  const int lane = threadIdx.x & 31;
+  double s = 0.0;
+  if (mine) {
+    if (p.renormalize && p.score == CHORD_SCORE_SOFTMAX) z = 1.0;  // cancels
+    s = score64(p, l, lmax, z);
+  }
+  if (p.renormalize) {
+    const double sum = warp_sum(s);
+    s = sum > 0.0 ? s / sum : 0.0;
+  }
+  if (mine) {
+    p.topk_ids[t * p.k + rank] = e;
+    p.topk_weights[t * p.k + rank] = float(s * double(p.scale));
+  }
+  for (int r = n + lane; r < p.k; r += 32) {
+    p.topk_ids[t * p.k + r] = -1;
+    p.topk_weights[t * p.k + r] = 0.f;
+  }
+}
+
+// Every c in FP64 (shared memory), k rounds of a warp-wide maximum.
+__device__ __noinline__ void route_exact(const RouterArgs& p, int64_t t, float lmax, double* c64) {
+  const int lane = threadIdx.x & 31;
+  const int per = (p.G + 31) / 32;
+  double z = 0.0;
+  if (p.score == CHORD_SCORE_SOFTMAX) {
+    z = softmax_sum64(p, t, lmax);
+  }
+  __syncwarp();
+  for (int e = lane; e < p.G; e += 32) {
+    const float l = load_logit(p, t * p.ld, e);
+    double c = -INFINITY;
+    if (l > -INFINITY) c = p.bias ? score64(p, l, lmax, z) + double(__ldg(p.bias + e)) : double(l);
+    c64[e] = c;
+  }
+  __syncwarp();
+  uint32_t kept = kFull;
+  if (p.n_group > 1) {
+    bool near;
+    kept = kept_groups<double>(p, c64, lmax, 0.0, 0.0, &near);
+  }
+  uint32_t open = 0;  // this lane's experts that may still be chosen
+  for (int i = 0; i < per; ++i) {
+    const int e = lane + 32 * i;
+    if (e < p.G && c64[e] > -INFINITY && (p.n_group == 1 || ((kept >> (e / p.group_size)) & 1u))) open |= 1u << i;
+  }
+  double sum = 0.0;
+  int n = 0;
+  for (; n < p.k; ++n) {
+    double best = -INFINITY;
+    int be = 0x7fffffff;
+    for (int i = 0; i < per; ++i)
+      if ((open >> i) & 1u) {
+        const double c = c64[lane + 32 * i];
+        if (c > best) {
+          best = c;
+          be = lane + 32 * i;
+        }
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double oc = __shfl_xor_sync(kFull, best, o);
+      const int oe = __shfl_xor_sync(kFull, be, o);
+      if (oc > best || (oc == best && oe < be)) {
+        best = oc;
+        be = oe;
+      }
+    }
+    if (be == 0x7fffffff) break;
+    if ((be & 31) == lane) open &= ~(1u << (be >> 5));
+    const double s = score64(p, load_logit(p, t * p.ld, be), lmax, p.renormalize ? 1.0 : z);
+    sum += s;
+    if (lane == 0) {
+      p.topk_ids[t * p.k + n] = be;
+      p.topk_weights[t * p.k + n] = float(s * double(p.scale));
+    }
+  }
+  __syncwarp();
+  for (int r = lane; r < p.k; r += 32) {
+    if (r >= n) {
+      p.topk_ids[t * p.k + r] = -1;
+      p.topk_weights[t * p.k + r] = 0.f;
+    } else if (p.renormalize) {
+      const int e = p.topk_ids[t * p.k + r];
+      const double s = score64(p, load_logit(p, t * p.ld, e), lmax, 1.0);
+      p.topk_weights[t * p.k + r] = sum > 0.0 ? float(s / sum * double(p.scale)) : 0.f;
+    }
+  }
+  __syncwarp();
+}
+
+// One token by one warp. `scratch`: G doubles, then 32 ints and 32 floats, of this warp.
+template <int PER>
+__device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint8_t* scratch) {
+  const int lane = threadIdx.x & 31;
+  double* c64 = reinterpret_cast<double*>(scratch);
+  float* c32 = reinterpret_cast<float*>(scratch);
+  int* cand_e = reinterpret_cast<int*>(scratch + size_t(p.G) * 8);
+  float* cand_l = reinterpret_cast<float*>(cand_e + 32);
+
+  float l[PER], c[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = e < p.G ? load_logit(p, t * p.ld, e) : -INFINITY;
+  }
+  float lmax = 0.f;
+  double z = 1.0;
+  if (p.score == CHORD_SCORE_SOFTMAX) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+    lmax = m > -INFINITY ? m : 0.f;
+    if (p.bias || !p.renormalize) {
+      float zf = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) zf += expf(l[i] - lmax);  // exp(-inf) = 0 for masked experts
+      zf = warp_sum(zf);
+      z = zf > 0.f ? double(zf) : 1.0;
+    }
+  }
+  if (p.bias) {
+    const float rz = 1.0f / float(z);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane + 32 * i;
+      float v = -INFINITY;
+      if (l[i] > -INFINITY) {
+        const float s = p.score == CHORD_SCORE_SIGMOID ? __fdividef(1.f, 1.f + __expf(-fminf(fmaxf(l[i], -80.f), 80.f)))
+                                                       : expf(l[i] - lmax) * rz;
+        v = s + __ldg(p.bias + e);
+      }
+      c[i] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] = l[i];
+  }
+
+  if (p.n_group > 1) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane + 32 * i;
+      if (e < p.G) c32[e] = c[i];
+    }
+    __syncwarp();
+    bool near;
+    const uint32_t kept = kept_groups<float>(p, c32, lmax, p.bias ? double(kSlackAbs) : 0.0,
+                                             p.bias ? double(kSlackRel) : 0.0, &near);
+    if (near && p.bias) {
+      route_exact(p, t, lmax, c64);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t g = uint32_t((uint64_t(lane + 32 * i) * p.group_magic) >> 32);
+      if (!((kept >> (g & 31)) & 1u)) c[i] = -INFINITY;
+    }
+  }
+
+  // threshold: the k-th largest lane maximum (all lanes that share a value count at once)
+  float thr = -INFINITY;
+  bool fits = p.k <= 32;
+  if (fits) {
+    float best = c[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) best = fmaxf(best, c[i]);
+    uint32_t key = order_key(best);
+    const uint32_t none = order_key(-INFINITY);
+    int seen = 0;
+    for (int r = 0; r < p.k; ++r) {
+      const uint32_t m = __reduce_max_sync(kFull, key);
+      if (m == none) break;
+      seen += __popc(__ballot_sync(kFull, key == m));
+      if (seen >= p.k) {
+        thr = order_value(m);
+        break;
+      }
+      if (key == m) key = none;
+    }
+    if (p.bias && thr > -INFINITY) thr -= kSlackAbs + kSlackRel * fabsf(thr);
+  }
+  int n = 0;
+  if (fits) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool in = c[i] >= thr && c[i] > -INFINITY;
+      const uint32_t who = __ballot_sync(kFull, in);
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      if (in && at < 32) {
+        cand_e[at] = lane + 32 * i;
+        cand_l[at] = l[i];
+      }
+      n += __popc(who);
+    }
+    fits = n <= 32;
+  }
+  if (!fits) {
+    route_exact(p, t, lmax, c64);
+    return;
+  }
+  __syncwarp();
+  // candidates stand in increasing id, so a tie goes to the lower lane
+  const bool mine = lane < n;
+  const int e = mine ? cand_e[lane] : 0;
+  const float lc = mine ? cand_l[lane] : 0.f;
+  __syncwarp();
+  double key = -INFINITY, gap;
+  if (mine) key = p.bias ? score64(p, lc, lmax, z) + double(__ldg(p.bias + e)) : double(lc);
+  int rank = rank_of(key, n, &gap);
+  if (p.bias && p.score == CHORD_SCORE_SOFTMAX && __any_sync(kFull, gap <= 2.0 * kSlackAbs)) {
+    // the denominator's FP32 error could swap two experts: once more with it in FP64
+    z = softmax_sum64(p, t, lmax);
+    if (mine) key = score64(p, lc, lmax, z) + double(__ldg(p.bias + e));
+    rank = rank_of(key, n, &gap);
+  }
+  write_token(p, t, mine && rank < p.k, rank, e, lc, lmax, z, n);
+}
+
+__host__ __device__ inline size_t router_scratch_bytes(int G) { return size_t(G) * 8 + 32 * 8; }
+
+template <int PER>
+__global__ void __launch_bounds__(32 * kRouterWarps) router_scored_kernel(const __grid_constant__ RouterArgs p) {
+  extern __shared__ __align__(16) uint8_t router_smem[];
+  const int warp = threadIdx.x >> 5;
+  uint8_t* scratch = router_smem + warp * router_scratch_bytes(p.G);
+  for (int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp; t < p.T; t += int64_t(gridDim.x) * kRouterWarps)
+    route_token<PER>(p, t, scratch);
+}
+
+// Up to kRouterWarps tokens: one CTA routes them, one warp each, then sorts the ids.
+template <int PER>
+__global__ void __launch_bounds__(1024) router_scored_align_kernel(const __grid_constant__ RouterArgs p, int E,
+                                                                   int block_m, int64_t cap, int64_t nblocks,
+                                                                   int32_t* __restrict__ sorted_ids,
+                                                                   int32_t* __restrict__ expert_ids,
+                                                                   int32_t* __restrict__ ntp,
+                                                                   int32_t* __restrict__ offsets) {
+  extern __shared__ __align__(16) uint8_t router_smem[];
+  const int warp = threadIdx.x >> 5;
+  if (warp < p.T) route_token<PER>(p, warp, router_smem + warp * router_scratch_bytes(p.G));
+  __syncthreads();
+  align_single_body(p.topk_ids, p.T * p.k, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets,
+                    reinterpret_cast<int*>(router_smem));
+}
+
+template <int PER>
+cudaError_t launch_per(const RouterArgs& p, int E, int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
+                       int32_t* expert_ids, int32_t* ntp, int32_t* offsets, void* workspace, int num_sms,
+                       cudaStream_t stream) {
+  const size_t route = router_scratch_bytes(p.G) * kRouterWarps;
+  if (p.T <= kRouterWarps) {
+    size_t smem = align_single_smem_bytes(E);
+    if (route > smem) smem = route;
+    cudaError_t err = cudaFuncSetAttribute(router_scored_align_kernel<PER>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (err != cudaSuccess) return err;
+    router_scored_align_kernel<PER><<<1, 1024, smem, stream>>>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids,
+                                                               ntp, offsets);
+    count_launches(1);
+    return cudaGetLastError();
+  }
+  cudaError_t err = cudaFuncSetAttribute(router_scored_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(route));
+  if (err != cudaSuccess) return err;
+  const int64_t want = (p.T + kRouterWarps - 1) / kRouterWarps, most = int64_t(num_sms) * 8;
+  router_scored_kernel<PER><<<unsigned(want < most ? want : most), 32 * kRouterWarps, route, stream>>>(p);
+  count_launches(1);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  return launch_align(p.topk_ids, p.T * p.k, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets,
+                      workspace, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_router_scored(const RouterArgs& p, int E, int block_m, int64_t cap, int64_t nblocks,
+                                 int32_t* sorted_ids, int32_t* expert_ids, int32_t* ntp, int32_t* offsets,
+                                 void* workspace, int num_sms, cudaStream_t stream) {
+  const int per = (p.G + 31) / 32;  // the smallest instantiated count that covers G
+  if (per <= 4)
+    return launch_per<4>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, workspace, num_sms, stream);
+  if (per <= 8)
+    return launch_per<8>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, workspace, num_sms, stream);
+  if (per <= 12)
+    return launch_per<12>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, workspace, num_sms, stream);
+  if (per <= 16)
+    return launch_per<16>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, workspace, num_sms, stream);
+  return launch_per<32>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, workspace, num_sms, stream);
+}
+
+}  // namespace chord
