@@ -54,5 +54,7 @@ struct Fp8QuantArgs {
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t stream);
 // Any number of rows; a.bm in {8, 16, 32}.
 cudaError_t launch_fp8_stream(const Fp8Args& a, cudaStream_t stream);
+// a.bm in {128, 256}: single CTAs or CTA pairs.
+cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream);
 
 }  // namespace chord

@@ -33,6 +33,7 @@ chord_status_t check_product(const uint8_t* xq, const float* xs, int64_t rows, i
   if (E < 1 || E > 1024) return fail(CHORD_ERR_UNSUPPORTED, "E=%d outside [1, 1024]", E);
   if (K < 16 || K % 16 || N < 8 || N % 8)
     return fail(CHORD_ERR_UNSUPPORTED, "K=%d must be a positive multiple of 16 and N=%d of 8", K, N);
+  if (int64_t(E) * N >= (int64_t(1) << 31)) return fail(CHORD_ERR_UNSUPPORTED, "E=%d times N=%d >= 2^31", E, N);
   const chord_status_t st = check_rows(rows);
   if (st != CHORD_OK) return st;
   if (flags & ~(CHORD_FLAG_FORCE_STREAM | CHORD_FLAG_FORCE_TENSOR | CHORD_FLAG_OUTPUT_FP32))
@@ -72,8 +73,8 @@ Fp8Args product_args(const uint8_t* xq, const float* xs, int64_t rows, int K, co
 // The schedule for `expected` rows per expert, then the product.
 chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices, const int32_t* masked_m,
                            int64_t max_m, void* workspace, int flags, cudaStream_t stream) {
-  (void)flags;
-  a.bm = expected <= 8 ? 8 : expected <= 16 ? 16 : 32;
+  const bool tensor = (flags & CHORD_FLAG_FORCE_TENSOR) || (!(flags & CHORD_FLAG_FORCE_STREAM) && expected > 32);
+  a.bm = tensor ? (expected > 128 ? 256 : 128) : (expected <= 8 ? 8 : expected <= 16 ? 16 : 32);
   cudaError_t err;
   if (a.layout != kFp8Dense) {
     const Fp8Workspace ws = fp8_workspace(a.rows, a.E);
@@ -90,8 +91,8 @@ chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices
     a.block_row0 = block_row0;
     a.sorted_ids = sorted_ids;
   }
-  err = launch_fp8_stream(a, stream);
-  return err == cudaSuccess ? CHORD_OK : cuda_fail(err, "FP8 streaming GEMM launch");
+  err = tensor ? launch_fp8_tile(a, stream) : launch_fp8_stream(a, stream);
+  return err == cudaSuccess ? CHORD_OK : cuda_fail(err, tensor ? "FP8 tensor-core GEMM launch" : "FP8 streaming GEMM launch");
 }
 
 chord_status_t quantize(const void* x, int dtype, int64_t ld, int64_t rows, int K, int silu, const int32_t* masked_m,

@@ -1,0 +1,443 @@
+// fp8_tile.cu -- FP8 block-128 products on the tensor cores (tcgen05) for many rows.
+//
+//   out[m, n] = sum_kb s[m, n/128, kb] * P_kb[m, n],   P_kb = xq[m, kb] . w[n, kb],
+//   s = xs[kb, m] * ws[n/128, kb]
+//
+// The FP32 scales are arbitrary, so the tensor core cannot apply them: it forms P_kb, the
+// product of one 128-wide k block, in tensor memory, and CUDA cores add s * P_kb to FP32
+// registers while it forms the next one in the other of two buffers. Activation rows are
+// the M side, so a thread owns one row and a block costs it one scale and one fused
+// multiply-add per column.
+//
+//   warp 0      TMA producer: per k block 128 activation rows and this CTA's weight rows,
+//               128 bytes wide (128-byte swizzle), into a ring of stages.
+//   warp 1      MMA issuer (one thread): four tcgen05.mma (K = 32) per k block, the first
+//               overwriting the buffer; commits free the stage and publish the buffer.
+//   warps 4..11 promotion: tcgen05.ld of the buffer (four warps per 32-lane quadrant pair,
+//               each half of the columns), FP32 accumulation in registers, output.
+//
+// CG = 2 runs a CTA pair (cta_group::2): M = 256, each CTA holding 128 activation rows and
+// half of the weight rows, so a CTA fetches 32 KiB per 256 x 256 x 128 step instead of 48:
+// at full rate 128 x 256 tiles of single CTAs would ask L2 for half as much again.
+//
+// Per k block of a 128 x 256 CTA tile the MMA takes 512 cycles (8192 FP8 multiply-adds a
+// cycle), the promotion 256 cycles of the FP32 pipe: the tensor core stays the bound.
+//
+// All waits are bounded. On a timeout a CTA raises CHORD_DEV_TIMEOUT, waits (bounded) for
+// its copies and MMAs in flight, frees its tensor memory and returns.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "fp8.cuh"
+#include "tc_common.cuh"
+
+namespace chord {
+namespace {
+
+constexpr int kPromoteWarps = 8;
+constexpr int kFirstPromoteWarp = 4;           // a warpgroup of its own for the producer and the MMA issuer
+constexpr int kTileThreads = 32 * (kFirstPromoteWarp + kPromoteWarps);
+constexpr int kBM = 128;                       // activation rows of a CTA
+constexpr int kABytes = kBM * kFp8Block;
+constexpr int kFixedBytes = 1024;              // barriers and the TMEM slot
+constexpr int kSmemBudget = 232448 - 1024 - kFixedBytes;  // 227 KiB less alignment slack
+
+template <int CG, int BN>
+struct TileCfg {
+  static constexpr int kBRows = BN / CG;
+  static constexpr int kStageBytes = kABytes + kBRows * kFp8Block;
+  static constexpr int kStages = kSmemBudget / kStageBytes > 8 ? 8 : kSmemBudget / kStageBytes;
+  static constexpr int kSmemBytes = 1024 + kFixedBytes + kStages * kStageBytes;
+  static constexpr int kCols = BN / 2;         // columns of a promotion warp
+};
+
+// Instruction descriptor, kind::f8f6f4: D f32, A and B e4m3, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on `bar` (in both CTAs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CG == 2)
+    tc2_commit_both(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tma_2d(uint32_t dst, const void* map, int k, int row, uint32_t bar) {
+  if (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row), "r"(bar)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+  if (CG == 2) {
+    tmem_alloc_pair(dst, cols);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
+  if (CG == 2)
+    tmem_dealloc_pair(base, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+
+// 32 lanes x 16 columns of tensor memory, without waiting.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+// Waits for it: the registers pass through, so no use of them can move ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t r[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::
+                   "memory");
+}
+
+// Registers per thread: 384 threads launch with 168 each (64512 together); a CTA tile with
+// 128 accumulators per thread takes 232 for its 256 promotion threads and leaves 40 to the
+// other 128 (59392 + 5120 = 64512).
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct TileMaps {
+  CUtensorMap x, w;
+};
+
+template <int CG, int BN>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    fp8_tile_kernel(const __grid_constant__ TileMaps maps, const Fp8Args p) {
+  using Cfg = TileCfg<CG, BN>;
+  constexpr int S = Cfg::kStages, COLS = Cfg::kCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [S] stage loaded (rank 0's is used)
+  uint64_t* empty = full + S;                          // [S] stage consumed
+  uint64_t* acc_full = empty + S;                      // [2] buffer holds a k block's product
+  uint64_t* acc_empty = acc_full + 2;                  // [2] buffer read by every warp (rank 0's is used)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kPromoteWarps * CG);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();  // the peer's barriers exist before anything arrives on them
+  if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  volatile int* abort_v = &abort_flag;
+
+  const int KB = fp8_blocks(p.K), NT = (p.N + BN - 1) / BN, NB = fp8_blocks(p.N);
+  const int64_t units = p.layout == kFp8Dense ? (p.rows + kBM * CG - 1) / (kBM * CG) : p.ntp[0] / (kBM * CG);
+  const int64_t tiles = units * NT;
+  const int64_t cid = CG == 2 ? cluster_id_x() : blockIdx.x, ncl = CG == 2 ? num_clusters_x() : gridDim.x;
+
+  if (warp < kFirstPromoteWarp) {
+    if (COLS == 128) give_registers<40>();
+    if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : smem_u32(full);
+      uint32_t fill = 0;
+      bool ok = true;
+      for (int64_t t = cid; t < tiles && ok; t += ncl) {
+        const int64_t u = t / NT;
+        const int nt = int(t - u * NT);
+        const int e = p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u);
+        const int row = (p.layout == kFp8Dense ? int(u * kBM * CG) : __ldg(p.block_row0 + u)) + int(rank) * kBM;
+        const int wrow = e * p.N + nt * BN + int(rank) * Cfg::kBRows;
+        for (int kb = 0; kb < KB; ++kb, ++fill) {
+          const uint32_t s = fill % S;
+          if (fill >= S && !mbar_wait(&empty[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * Cfg::kStageBytes);
+          const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes;
+          tma_2d<CG>(st, &maps.x, kb * kFp8Block, row, full0 + s * 8);
+          tma_2d<CG>(st + kABytes, &maps.w, kb * kFp8Block, wrow, full0 + s * 8);
+        }
+      }
+      // the last copies have landed before the CTA ends (rank 0's barriers count both CTAs')
+      if (rank == 0) {
+        int dummy = 0;
+        for (uint32_t f = fill > S ? fill - S : 0; f < fill; ++f) mbar_wait(&full[f % S], (f / S) & 1, &dummy, p.status);
+      }
+    }
+    __syncwarp();
+    } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(kBM * CG, BN);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t t = cid; t < tiles && ok; t += ncl) {
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const uint32_t s = it % S, b = it & 1;
+          if ((it >= 2 && !mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1, abort_v, p.status)) ||
+              !mbar_wait(&full[s], (it / S) & 1, abort_v, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes;
+          const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kABytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_e4m3<CG>(tmem + b * BN, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+          commit<CG>(&empty[s]);
+          commit<CG>(&acc_full[b]);
+        }
+      }
+      if (it > 0) {  // no MMA writes tensor memory once it is freed
+        int dummy = 0;
+        mbar_wait(&empty[(it - 1) % S], ((it - 1) / S) & 1, &dummy, p.status);
+      }
+    }
+    __syncwarp();
+    }
+  } else {
+    if (COLS == 128) take_registers<232>();
+    const int q = warp & 3;            // the tensor-memory lanes this warp may read
+    const int h = (warp - kFirstPromoteWarp) >> 2;     // its half of the columns
+    const int r = q * 32 + lane;
+    const uint32_t empty0 = CG == 2 ? cluster_addr(acc_empty, 0) : smem_u32(acc_empty);
+    const uint32_t src = tmem + (uint32_t(q * 32) << 16) + h * COLS;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t t = cid; t < tiles && ok; t += ncl) {
+      const int64_t u = t / NT;
+      const int n0 = int(t - u * NT) * BN + h * COLS;
+      const int e = p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u);
+      const int64_t row = (p.layout == kFp8Dense ? u * kBM * CG : int64_t(__ldg(p.block_row0 + u))) + rank * kBM + r;
+      const bool live = p.layout == kFp8Dense ? row < p.rows
+                                              : __ldg(p.sorted_ids + u * kBM * CG + rank * kBM + r) >= 0;
+      // scales: one per row (rows that are not stored read row 0's), one for the columns
+      const float* xs = p.xs + (row < p.rows ? row : 0);
+      const int nb = min(n0 / kFp8Block, NB - 1);
+      const float* ws = p.ws + (int64_t(e) * NB + nb) * KB;
+      float acc[COLS];
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
+      constexpr int G = 4;  // k blocks whose scales are loaded together, a group ahead
+      float sx[G], sw[G];
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        sx[i] = i < KB ? __ldg(xs + i * p.rows) : 0.f;
+        sw[i] = i < KB ? __ldg(ws + i) : 0.f;
+      }
+      for (int kb0 = 0; kb0 < KB && ok; kb0 += G) {
+        float nx[G], nw[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const int kb = kb0 + G + i;
+          nx[i] = kb < KB ? __ldg(xs + kb * p.rows) : 0.f;
+          nw[i] = kb < KB ? __ldg(ws + kb) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          if (kb0 + i >= KB) break;
+          const uint32_t b = it & 1;
+          if (!mbar_wait(&acc_full[b], (it >> 1) & 1, abort_v, p.status)) {
+            ok = false;
+            break;
+          }
+          ++it;
+          tc_fence_after();
+          const float s = sx[i] * sw[i];
+          uint32_t v[2][16];
+          tmem_ld16_async(src + b * BN, v[0]);
+#pragma unroll
+          for (int c = 0; c < COLS / 16; ++c) {
+            tmem_wait_ld16(v[c & 1]);
+            if (c + 1 < COLS / 16) tmem_ld16_async(src + b * BN + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[16 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, acc[16 * c + j]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2) mbar_arrive_cluster(empty0 + b * 8);
+            else mbar_arrive(&acc_empty[b]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          sx[i] = nx[i];
+          sw[i] = nw[i];
+        }
+      }
+      if (!ok || !live) continue;
+      if (p.out_f32) {
+        float* o = static_cast<float*>(p.out) + row * p.N + n0;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 4)
+          if (n0 + c < p.N) *reinterpret_cast<float4*>(o + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+      } else {
+        uint16_t* o = static_cast<uint16_t*>(p.out) + row * p.N + n0;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 8)
+          if (n0 + c < p.N) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(acc[c + 2 * j], acc[c + 2 * j + 1]);
+              w[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();  // nothing of either CTA is in flight towards the other
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<CG>(tmem, 2 * BN);
+  }
+}
+
+// ------------------------------------------------------------------------------------ host
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiledFn>(nullptr);
+    return reinterpret_cast<EncodeTiledFn>(ptr);
+  }();
+  return fn;
+}
+
+// Codes [rows, K], boxes of 128 columns x box_rows rows; what lies outside reads as zero.
+cudaError_t code_map(CUtensorMap* map, const void* base, int64_t rows, int K, int box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(K)};
+  const cuuint32_t box[2] = {kFp8Block, cuuint32_t(box_rows)}, one[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int CG, int BN>
+cudaError_t launch(const Fp8Args& a, cudaStream_t stream) {
+  using Cfg = TileCfg<CG, BN>;
+  auto kern = fp8_tile_kernel<CG, BN>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // clusters that fit at once, per device (they must fit inside a GPC)
+  static std::mutex mu;
+  static int fits[64];
+  int dev = 0;
+  if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int most;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (fits[dev] == 0) {
+      cfg.gridDim = dim3(unsigned(a.num_sms / CG * CG));
+      if ((err = cudaOccupancyMaxActiveClusters(&fits[dev], kern, &cfg)) != cudaSuccess) return err;
+    }
+    most = fits[dev];
+  }
+  if (most < 1) return cudaErrorLaunchOutOfResources;
+  if (most > a.num_sms / CG) most = a.num_sms / CG;
+  TileMaps maps;
+  if ((err = code_map(&maps.x, a.xq, a.rows, a.K, kBM)) != cudaSuccess) return err;
+  if ((err = code_map(&maps.w, a.w, int64_t(a.E) * a.N, a.K, Cfg::kBRows)) != cudaSuccess) return err;
+  // upper bound of the tiles (the grouped unit count is on the device)
+  const int64_t units = (a.rows + kBM * CG - 1) / (kBM * CG) + (a.layout == kFp8Dense ? 0 : a.E);
+  const int64_t tiles = units * ((a.N + BN - 1) / BN);
+  cfg.gridDim = dim3(unsigned((tiles < most ? tiles : most) * CG));
+  err = cudaLaunchKernelEx(&cfg, kern, maps, a);
+  count_launches(1);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream) {
+  return a.bm == 256 ? launch<2, 256>(a, stream) : launch<1, 128>(a, stream);
+}
+
+}  // namespace chord
