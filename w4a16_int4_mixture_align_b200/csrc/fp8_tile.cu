@@ -9,8 +9,9 @@
 // the M side, so a thread owns one row and a block costs it one scale and one fused
 // multiply-add per column.
 //
-//   warp 0      TMA producer: per k block 128 activation rows and this CTA's weight rows,
-//               128 bytes wide (128-byte swizzle), into a ring of stages.
+//   warps 0, 2  TMA producers: per k block 128 activation rows (warp 0) and this CTA's
+//               weight rows (warp 2), 128 bytes wide (128-byte swizzle), into a ring of
+//               stages.
 //   warp 1      MMA issuer (one thread): four tcgen05.mma (K = 32) per k block, the first
 //               overwriting the buffer; commits free the stage and publish the buffer.
 //   warps 4..11 promotion: tcgen05.ld of the buffer (four warps per 32-lane quadrant pair,
@@ -38,17 +39,19 @@ namespace {
 constexpr int kPromoteWarps = 8;
 constexpr int kFirstPromoteWarp = 4;           // a warpgroup of its own for the producer and the MMA issuer
 constexpr int kTileThreads = 32 * (kFirstPromoteWarp + kPromoteWarps);
+constexpr int kChunkCols = 16;                 // columns of a tensor-memory load
 constexpr int kBM = 128;                       // activation rows of a CTA
 constexpr int kABytes = kBM * kFp8Block;
 constexpr int kFixedBytes = 1024;              // barriers and the TMEM slot
-constexpr int kSmemBudget = 232448 - 1024 - kFixedBytes;  // 227 KiB less alignment slack
+constexpr int kOutBytes = kPromoteWarps * 4096;  // output staging
+constexpr int kSmemBudget = 232448 - 1024 - kFixedBytes - kOutBytes;  // 227 KiB less alignment slack
 
 template <int CG, int BN>
 struct TileCfg {
   static constexpr int kBRows = BN / CG;
   static constexpr int kStageBytes = kABytes + kBRows * kFp8Block;
   static constexpr int kStages = kSmemBudget / kStageBytes > 8 ? 8 : kSmemBudget / kStageBytes;
-  static constexpr int kSmemBytes = 1024 + kFixedBytes + kStages * kStageBytes;
+  static constexpr int kSmemBytes = 1024 + kFixedBytes + kStages * kStageBytes + kOutBytes;
   static constexpr int kCols = BN / 2;         // columns of a promotion warp
 };
 
@@ -117,25 +120,44 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
 
-// 32 lanes x 16 columns of tensor memory, without waiting.
-__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, uint32_t r[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
+// 32 lanes x W columns of tensor memory, without waiting.
+__device__ __forceinline__ void tmem_ld_async(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
 }
-// Waits for it: the registers pass through, so no use of them can move ahead of the wait.
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t r[16]) {
+__device__ __forceinline__ void tmem_ld_async(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(addr));
+}
+// Waits for the loads so far; the registers pass through, so no use of them can move ahead.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::
-                   "memory");
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// Registers per thread: 384 threads launch with 168 each (64512 together); a CTA tile with
-// 128 accumulators per thread takes 232 for its 256 promotion threads and leaves 40 to the
-// other 128 (59392 + 5120 = 64512).
+// a += (x0, x1) * (s, s): two FP32 fused multiply-adds, each rounded as by fmaf.
+__device__ __forceinline__ void fma2(uint64_t& a, uint32_t x0, uint32_t x1, uint64_t s) {
+  asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tfma.rn.f32x2 %0, x, %3, %0;\n\t}"
+      : "+l"(a)
+      : "r"(x0), "r"(x1), "l"(s));
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// Registers per thread: 384 threads launch with 168 each (64512 together); the 256 promotion
+// threads take 232 and leave 40 to the other 128 (59392 + 5120 = 64512).
 template <int N>
 __device__ __forceinline__ void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -146,8 +168,48 @@ __device__ __forceinline__ void give_registers() {
 }
 
 struct TileMaps {
-  CUtensorMap x, w;
+  CUtensorMap x, w, out;
 };
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A warp's 32 rows (one per lane) x COLS columns to the output, in boxes of 32 rows x 128
+// bytes staged in `buf` (4 KiB, 1024-byte aligned, 128-byte swizzle so that the eight lanes
+// of a store phase hit different banks).
+constexpr int kStagingBytes = 4096;
+template <int COLS, bool F32>
+__device__ __forceinline__ void store_rows(const CUtensorMap& map, const float (&acc)[COLS], uint32_t buf, int n0,
+                                           int row0, int N) {
+  constexpr int W = F32 ? 32 : 64;  // columns of a box
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < COLS; c += W) {
+    if (n0 + c >= N) break;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // `buf` is free again
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = F32 ? __float_as_uint(acc[c + 4 * j + (F32 ? i : 0)])
+                   : bf16_pair(acc[c + (F32 ? 0 : 8 * j + 2 * i)], acc[c + (F32 ? 0 : 8 * j + 2 * i + 1)]);
+      sts128(buf + lane * 128 + ((j ^ (lane & 7)) << 4), v);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                       reinterpret_cast<uint64_t>(&map)),
+                   "r"(n0 + c), "r"(row0), "r"(buf)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  }
+}
 
 template <int CG, int BN>
 __global__ void __launch_bounds__(kTileThreads, 1)
@@ -188,48 +250,51 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile int* abort_v = &abort_flag;
 
   const int KB = fp8_blocks(p.K), NT = (p.N + BN - 1) / BN, NB = fp8_blocks(p.N);
-  const int64_t units = p.layout == kFp8Dense ? (p.rows + kBM * CG - 1) / (kBM * CG) : p.ntp[0] / (kBM * CG);
-  const int64_t tiles = units * NT;
-  const int64_t cid = CG == 2 ? cluster_id_x() : blockIdx.x, ncl = CG == 2 ? num_clusters_x() : gridDim.x;
+  // 32 bits: the host checks that the tiles' number fits
+  const int units = p.layout == kFp8Dense ? int((p.rows + kBM * CG - 1) / (kBM * CG)) : p.ntp[0] / (kBM * CG);
+  const int tiles = units * NT;
+  const int cid = CG == 2 ? cluster_id_x() : blockIdx.x, ncl = CG == 2 ? num_clusters_x() : gridDim.x;
 
   if (warp < kFirstPromoteWarp) {
-    if (COLS == 128) give_registers<40>();
-    if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : smem_u32(full);
-      uint32_t fill = 0;
-      bool ok = true;
-      for (int64_t t = cid; t < tiles && ok; t += ncl) {
-        const int64_t u = t / NT;
-        const int nt = int(t - u * NT);
-        const int e = p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u);
-        const int row = (p.layout == kFp8Dense ? int(u * kBM * CG) : __ldg(p.block_row0 + u)) + int(rank) * kBM;
-        const int wrow = e * p.N + nt * BN + int(rank) * Cfg::kBRows;
-        for (int kb = 0; kb < KB; ++kb, ++fill) {
-          const uint32_t s = fill % S;
-          if (fill >= S && !mbar_wait(&empty[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
-            ok = false;
-            break;
+    give_registers<40>();
+    if (warp == 0 || warp == 2) {
+      // warp 0 copies activation rows, warp 2 weight rows
+      if (lane == 0) {
+        const bool of_x = warp == 0;
+        const CUtensorMap* map = of_x ? &maps.x : &maps.w;
+        const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : smem_u32(full);
+        const uint32_t dst = sbase + kFixedBytes + (of_x ? 0 : kABytes);
+        uint32_t fill = 0;
+        bool ok = true;
+        for (int t = cid; t < tiles && ok; t += ncl) {
+          const int u = t / NT, nt = t - u * NT;
+          int row;
+          if (of_x) row = (p.layout == kFp8Dense ? u * kBM * CG : __ldg(p.block_row0 + u)) + int(rank) * kBM;
+          else row = (p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u)) * p.N + nt * BN + int(rank) * Cfg::kBRows;
+          for (int kb = 0; kb < KB; ++kb, ++fill) {
+            const uint32_t s = fill % S;
+            if (fill >= S && !mbar_wait(&empty[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0 && of_x) mbar_arrive_expect_tx(&full[s], CG * Cfg::kStageBytes);
+            tma_2d<CG>(dst + s * Cfg::kStageBytes, map, kb * kFp8Block, row, full0 + s * 8);
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * Cfg::kStageBytes);
-          const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes;
-          tma_2d<CG>(st, &maps.x, kb * kFp8Block, row, full0 + s * 8);
-          tma_2d<CG>(st + kABytes, &maps.w, kb * kFp8Block, wrow, full0 + s * 8);
+        }
+        // the last copies have landed before the CTA ends (rank 0's barriers count both CTAs')
+        if (rank == 0 && of_x) {
+          int dummy = 0;
+          for (uint32_t f = fill > S ? fill - S : 0; f < fill; ++f)
+            mbar_wait(&full[f % S], (f / S) & 1, &dummy, p.status);
         }
       }
-      // the last copies have landed before the CTA ends (rank 0's barriers count both CTAs')
-      if (rank == 0) {
-        int dummy = 0;
-        for (uint32_t f = fill > S ? fill - S : 0; f < fill; ++f) mbar_wait(&full[f % S], (f / S) & 1, &dummy, p.status);
-      }
-    }
-    __syncwarp();
+      __syncwarp();
     } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = idesc_e4m3(kBM * CG, BN);
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t t = cid; t < tiles && ok; t += ncl) {
+      for (int t = cid; t < tiles && ok; t += ncl) {
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const uint32_t s = it % S, b = it & 1;
           if ((it >= 2 && !mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1, abort_v, p.status)) ||
@@ -254,97 +319,109 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncwarp();
     }
   } else {
-    if (COLS == 128) take_registers<232>();
+    take_registers<232>();
     const int q = warp & 3;            // the tensor-memory lanes this warp may read
     const int h = (warp - kFirstPromoteWarp) >> 2;     // its half of the columns
     const int r = q * 32 + lane;
     const uint32_t empty0 = CG == 2 ? cluster_addr(acc_empty, 0) : smem_u32(acc_empty);
     const uint32_t src = tmem + (uint32_t(q * 32) << 16) + h * COLS;
+    const uint32_t staging = sbase + kFixedBytes + S * Cfg::kStageBytes + (warp - kFirstPromoteWarp) * kStagingBytes;
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t t = cid; t < tiles && ok; t += ncl) {
-      const int64_t u = t / NT;
-      const int n0 = int(t - u * NT) * BN + h * COLS;
+    for (int t = cid; t < tiles && ok; t += ncl) {
+      const int u = t / NT;
+      const int n0 = (t - u * NT) * BN + h * COLS;
       const int e = p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u);
-      const int64_t row = (p.layout == kFp8Dense ? u * kBM * CG : int64_t(__ldg(p.block_row0 + u))) + rank * kBM + r;
-      const bool live = p.layout == kFp8Dense ? row < p.rows
-                                              : __ldg(p.sorted_ids + u * kBM * CG + rank * kBM + r) >= 0;
+      const int pos = u * kBM * CG + int(rank) * kBM + r;
+      const int64_t row = p.layout == kFp8Dense ? pos : __ldg(p.block_row0 + u) + int(rank) * kBM + r;
+      const bool live = p.layout == kFp8Dense ? row < p.rows : __ldg(p.sorted_ids + pos) >= 0;
       // scales: one per row (rows that are not stored read row 0's), one for the columns
       const float* xs = p.xs + (row < p.rows ? row : 0);
       const int nb = min(n0 / kFp8Block, NB - 1);
       const float* ws = p.ws + (int64_t(e) * NB + nb) * KB;
+      uint64_t sum[COLS / 2];  // columns 2i, 2i + 1
+#pragma unroll
+      for (int c = 0; c < COLS / 2; ++c) sum[c] = 0;
+      // the scales of this k block and the next two (loads run two blocks ahead)
+      float x0 = __ldg(xs), w0 = __ldg(ws), x1 = 0.f, w1 = 0.f;
+      if (KB > 1) {
+        xs += p.rows;
+        x1 = __ldg(xs);
+        w1 = __ldg(ws + 1);
+      }
+      // the tensor-memory loads run one chunk of columns ahead of the additions, across k
+      // blocks too
+      constexpr int W = kChunkCols, CH = COLS / W;
+      uint32_t v[2][W];
+      ok = mbar_wait(&acc_full[it & 1], (it >> 1) & 1, abort_v, p.status);
+      tc_fence_after();
+      tmem_ld_async(src + (it & 1) * BN, v[0]);
+#pragma unroll 1
+      for (int kb = 0; kb < KB; ++kb) {
+        const float scale = x0 * w0;
+        const uint64_t s = pack2(scale, scale);
+        x0 = x1;
+        w0 = w1;
+        if (kb + 2 < KB) {
+          xs += p.rows;
+          x1 = __ldg(xs);
+          w1 = __ldg(ws + kb + 2);
+        }
+        const uint32_t b = it & 1;
+        ++it;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          tmem_wait_ld(v[c & 1]);
+          if (c + 1 < CH) {
+            tmem_ld_async(src + b * BN + W * (c + 1), v[(c + 1) & 1]);
+          } else {  // the buffer is read: hand it back, and request the next one's first chunk
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 2) mbar_arrive_cluster(empty0 + b * 8);
+              else mbar_arrive(&acc_empty[b]);
+            }
+            if (kb + 1 < KB) ok = ok && mbar_wait(&acc_full[it & 1], (it >> 1) & 1, abort_v, p.status);
+            tc_fence_after();
+            // after the last block this rereads a buffer of this CTA, for nothing
+            tmem_ld_async(src + (it & 1) * BN, v[0]);
+          }
+#pragma unroll
+          for (int j = 0; j < W; j += 2) fma2(sum[(W * c + j) / 2], v[c & 1][j], v[c & 1][j + 1], s);
+        }
+        if (!ok) break;
+      }
+      tmem_wait_ld(v[0]);
+      if (!ok) continue;
       float acc[COLS];
 #pragma unroll
-      for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
-      constexpr int G = 4;  // k blocks whose scales are loaded together, a group ahead
-      float sx[G], sw[G];
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        sx[i] = i < KB ? __ldg(xs + i * p.rows) : 0.f;
-        sw[i] = i < KB ? __ldg(ws + i) : 0.f;
-      }
-      for (int kb0 = 0; kb0 < KB && ok; kb0 += G) {
-        float nx[G], nw[G];
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          const int kb = kb0 + G + i;
-          nx[i] = kb < KB ? __ldg(xs + kb * p.rows) : 0.f;
-          nw[i] = kb < KB ? __ldg(ws + kb) : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          if (kb0 + i >= KB) break;
-          const uint32_t b = it & 1;
-          if (!mbar_wait(&acc_full[b], (it >> 1) & 1, abort_v, p.status)) {
-            ok = false;
-            break;
-          }
-          ++it;
-          tc_fence_after();
-          const float s = sx[i] * sw[i];
-          uint32_t v[2][16];
-          tmem_ld16_async(src + b * BN, v[0]);
-#pragma unroll
-          for (int c = 0; c < COLS / 16; ++c) {
-            tmem_wait_ld16(v[c & 1]);
-            if (c + 1 < COLS / 16) tmem_ld16_async(src + b * BN + 16 * (c + 1), v[(c + 1) & 1]);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) acc[16 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, acc[16 * c + j]);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 2) mbar_arrive_cluster(empty0 + b * 8);
-            else mbar_arrive(&acc_empty[b]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          sx[i] = nx[i];
-          sw[i] = nw[i];
-        }
-      }
-      if (!ok || !live) continue;
-      if (p.out_f32) {
+      for (int c = 0; c < COLS / 2; ++c) unpack2(sum[c], acc[2 * c], acc[2 * c + 1]);
+      // 32 whole rows leave through shared memory by TMA, 128 bytes wide, while the next tile
+      // runs (stores of a row per lane held the promotion for about 4 us a tile); rows past a
+      // dense matrix are cut off by the copy. Where some rows are not to be written, each lane
+      // stores its own.
+      const bool whole = p.layout == kFp8Dense || __all_sync(0xffffffffu, live);
+      if (whole) {
+        const int row0 = int(row) - lane;
+        if (row0 >= p.rows) continue;
+        if (p.out_f32) store_rows<COLS, true>(maps.out, acc, staging, n0, row0, p.N);
+        else store_rows<COLS, false>(maps.out, acc, staging, n0, row0, p.N);
+      } else if (live && p.out_f32) {
         float* o = static_cast<float*>(p.out) + row * p.N + n0;
 #pragma unroll
         for (int c = 0; c < COLS; c += 4)
           if (n0 + c < p.N) *reinterpret_cast<float4*>(o + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-      } else {
+      } else if (live) {
         uint16_t* o = static_cast<uint16_t*>(p.out) + row * p.N + n0;
 #pragma unroll
         for (int c = 0; c < COLS; c += 8)
-          if (n0 + c < p.N) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(acc[c + 2 * j], acc[c + 2 * j + 1]);
-              w[j] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          if (n0 + c < p.N)
+            *reinterpret_cast<uint4*>(o + c) = make_uint4(bf16_pair(acc[c], acc[c + 1]), bf16_pair(acc[c + 2], acc[c + 3]),
+                                                          bf16_pair(acc[c + 4], acc[c + 5]), bf16_pair(acc[c + 6], acc[c + 7]));
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -374,15 +451,17 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Codes [rows, K], boxes of 128 columns x box_rows rows; what lies outside reads as zero.
-cudaError_t code_map(CUtensorMap* map, const void* base, int64_t rows, int K, int box_rows) {
+// A row-major matrix [rows, cols] of `size`-byte elements, boxes of 128 bytes x box_rows rows
+// (128-byte swizzle); what lies outside reads as zero and is not written.
+cudaError_t matrix_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t rows, int cols,
+                       int box_rows) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
-  const cuuint64_t strides[1] = {cuuint64_t(K)};
-  const cuuint32_t box[2] = {kFp8Block, cuuint32_t(box_rows)}, one[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(cols) * size};
+  const cuuint32_t box[2] = {cuuint32_t(128 / size), cuuint32_t(box_rows)}, one[2] = {1, 1};
+  return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
@@ -423,11 +502,16 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t stream) {
   if (most < 1) return cudaErrorLaunchOutOfResources;
   if (most > a.num_sms / CG) most = a.num_sms / CG;
   TileMaps maps;
-  if ((err = code_map(&maps.x, a.xq, a.rows, a.K, kBM)) != cudaSuccess) return err;
-  if ((err = code_map(&maps.w, a.w, int64_t(a.E) * a.N, a.K, Cfg::kBRows)) != cudaSuccess) return err;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if ((err = matrix_map(&maps.x, u8, 1, a.xq, a.rows, a.K, kBM)) != cudaSuccess) return err;
+  if ((err = matrix_map(&maps.w, u8, 1, a.w, int64_t(a.E) * a.N, a.K, Cfg::kBRows)) != cudaSuccess) return err;
+  err = matrix_map(&maps.out, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   a.out_f32 ? 4 : 2, a.out, a.rows, a.N, 32);
+  if (err != cudaSuccess) return err;
   // upper bound of the tiles (the grouped unit count is on the device)
   const int64_t units = (a.rows + kBM * CG - 1) / (kBM * CG) + (a.layout == kFp8Dense ? 0 : a.E);
   const int64_t tiles = units * ((a.N + BN - 1) / BN);
+  if (tiles >= int64_t(1) << 30) return cudaErrorInvalidValue;
   cfg.gridDim = dim3(unsigned((tiles < most ? tiles : most) * CG));
   err = cudaLaunchKernelEx(&cfg, kern, maps, a);
   count_launches(1);
