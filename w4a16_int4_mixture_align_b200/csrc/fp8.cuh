@@ -36,6 +36,7 @@ struct Fp8Args {
   int bm;
   uint32_t* status;
   int num_sms;
+  float* out_scales;  // gate_up: scales of the codes in `out`
 };
 
 struct Fp8QuantArgs {
@@ -51,10 +52,35 @@ struct Fp8QuantArgs {
   int num_sms;
 };
 
+// ---- quantisation of a block (used where rows are quantised and where a product ends in it)
+
+// Two FP32 to two E4M3 codes, nearest even, saturating; NaN stays NaN. lo is the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+// The scale of a block and its inverse from the bits of its largest |x| (as integers a NaN is
+// above infinity, infinity above the rest; both give a NaN scale).
+__device__ __forceinline__ void block_scale(uint32_t amax_bits, float* scale, float* inverse) {
+  const float amax = fmaxf(__uint_as_float(amax_bits), 0x1p-100f);
+  const float nan = __uint_as_float(0x7fffffffu);
+  const bool finite = amax_bits < 0x7f800000u;
+  *scale = finite ? __fdiv_rn(amax, kFp8Max) : nan;
+  *inverse = finite ? __fdiv_rn(kFp8Max, amax) : nan;
+}
+__device__ __forceinline__ float silu_times(float g, float u) { return __fdiv_rn(g, 1.f + expf(-g)) * u; }
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t stream);
 // Any number of rows; a.bm in {8, 16, 32}.
 cudaError_t launch_fp8_stream(const Fp8Args& a, cudaStream_t stream);
 // a.bm in {128, 256}: single CTAs or CTA pairs.
 cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream);
+// Dense, w = [gate; up] with a.N = 2 I: SiLU(gate) * up quantised to q [rows, I], scales [I/128, rows].
+cudaError_t launch_fp8_tile_gate_up(const Fp8Args& a, cudaStream_t stream);
 
 }  // namespace chord

@@ -95,6 +95,13 @@ chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices
   return err == cudaSuccess ? CHORD_OK : cuda_fail(err, tensor ? "FP8 tensor-core GEMM launch" : "FP8 streaming GEMM launch");
 }
 
+// One kernel for gate_up once its 256-row x 128-column tiles cover the CTA pairs; below, the
+// product of twice as many tiles (or the weight streaming) and a quantisation are faster.
+bool fused_gate_up(int64_t M, int I, int num_sms, int flags) {
+  if (flags & CHORD_FLAG_FORCE_STREAM) return false;
+  return (flags & CHORD_FLAG_FORCE_TENSOR) || (M + 255) / 256 * (I / kFp8Block) >= num_sms / 2;
+}
+
 chord_status_t quantize(const void* x, int dtype, int64_t ld, int64_t rows, int K, int silu, const int32_t* masked_m,
                         int E, uint8_t* q, float* scales, cudaStream_t stream) {
   if (K < 16 || K % 16 || K >= (1 << 30))
@@ -229,12 +236,17 @@ chord_status_t chord_fp8_gate_up(const uint8_t* xq, const float* xs, int64_t M, 
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != CHORD_OK) return st;
   if (M == 0) return CHORD_OK;
-  float* h = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + chord_fp8_workspace_bytes(M, 1));
-  st = run_product(product_args(xq, xs, M, H, w13, ws13, 1, 2 * I, h, workspace, flags | CHORD_FLAG_OUTPUT_FP32,
-                                kFp8Dense, num_sms),
-                   M, nullptr, nullptr, 0, workspace, flags, reinterpret_cast<cudaStream_t>(stream));
+  Fp8Args a = product_args(xq, xs, M, H, w13, ws13, 1, 2 * I, q, workspace, flags, kFp8Dense, num_sms);
+  if (fused_gate_up(M, I, num_sms, flags)) {
+    a.out_scales = scales;
+    const cudaError_t err = launch_fp8_tile_gate_up(a, reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? CHORD_OK : cuda_fail(err, "FP8 gate_up launch");
+  }
+  a.out = static_cast<uint8_t*>(workspace) + chord_fp8_workspace_bytes(M, 1);
+  a.out_f32 = 1;
+  st = run_product(a, M, nullptr, nullptr, 0, workspace, flags, reinterpret_cast<cudaStream_t>(stream));
   if (st != CHORD_OK) return st;
-  return quantize(h, CHORD_DTYPE_F32, 2 * int64_t(I), M, I, 1, nullptr, 0, q, scales,
+  return quantize(a.out, CHORD_DTYPE_F32, 2 * int64_t(I), M, I, 1, nullptr, 0, q, scales,
                   reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -37,13 +37,6 @@ __device__ __forceinline__ void load8(const void* base, int dtype, int64_t at, f
   }
 }
 
-// Two FP32 to two E4M3 codes, nearest even, saturating; NaN stays NaN. lo is the low byte.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 template <int DTYPE, bool SILU>
 __global__ void __launch_bounds__(32 * kQuantWarps) fp8_quantize_kernel(const Fp8QuantArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -82,23 +75,17 @@ __global__ void __launch_bounds__(32 * kQuantWarps) fp8_quantize_kernel(const Fp
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (SILU) {
-          const float g = v[s][i];
-          v[s][i] = __fdiv_rn(g, 1.f + expf(-g)) * up[SILU ? s : 0][i];
-        }
-        m = max(m, __float_as_uint(v[s][i]) & 0x7fffffffu);
+        if (SILU) v[s][i] = silu_times(v[s][i], up[SILU ? s : 0][i]);
+        m = max(m, abs_bits(v[s][i]));
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float amax = fmaxf(__uint_as_float(m), 0x1p-100f);
-      const bool finite = m < 0x7f800000u;
-      const float nan = __uint_as_float(0x7fffffffu);
-      const float scale = finite ? __fdiv_rn(amax, kFp8Max) : nan;
-      const float r = finite ? __fdiv_rn(kFp8Max, amax) : nan;
+      float scale, r;
+      block_scale(m, &scale, &r);
       if (c < a.K) {
         uint2 code;
-        code.x = e4m3x2(v[s][0] * r, v[s][1] * r) | (e4m3x2(v[s][2] * r, v[s][3] * r) << 16);
-        code.y = e4m3x2(v[s][4] * r, v[s][5] * r) | (e4m3x2(v[s][6] * r, v[s][7] * r) << 16);
+        code.x = e4m3x4(v[s][0] * r, v[s][1] * r, v[s][2] * r, v[s][3] * r);
+        code.y = e4m3x4(v[s][4] * r, v[s][5] * r, v[s][6] * r, v[s][7] * r);
         *reinterpret_cast<uint2*>(a.q + row * a.K + c) = code;
         if ((lane & 15) == 0) a.scales[int64_t(c / kFp8Block) * a.rows + row] = scale;
       }

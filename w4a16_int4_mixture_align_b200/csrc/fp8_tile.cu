@@ -43,7 +43,8 @@ constexpr int kChunkCols = 16;                 // columns of a tensor-memory loa
 constexpr int kBM = 128;                       // activation rows of a CTA
 constexpr int kABytes = kBM * kFp8Block;
 constexpr int kFixedBytes = 1024;              // barriers and the TMEM slot
-constexpr int kOutBytes = kPromoteWarps * 4096;  // output staging
+constexpr int kStagingBytes = 4096;            // output staging of a promotion warp
+constexpr int kOutBytes = kPromoteWarps * kStagingBytes;
 constexpr int kSmemBudget = 232448 - 1024 - kFixedBytes - kOutBytes;  // 227 KiB less alignment slack
 
 template <int CG, int BN>
@@ -176,10 +177,18 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// One thread: the staged box to the matrix at column `col`, row `row`.
+__device__ __forceinline__ void store_box(const CUtensorMap& map, int col, int row, uint32_t buf) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(&map)),
+               "r"(col), "r"(row), "r"(buf)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 // A warp's 32 rows (one per lane) x COLS columns to the output, in boxes of 32 rows x 128
-// bytes staged in `buf` (4 KiB, 1024-byte aligned, 128-byte swizzle so that the eight lanes
+// bytes staged in `buf` (1024-byte aligned, 128-byte swizzle so that the eight lanes
 // of a store phase hit different banks).
-constexpr int kStagingBytes = 4096;
 template <int COLS, bool F32>
 __device__ __forceinline__ void store_rows(const CUtensorMap& map, const float (&acc)[COLS], uint32_t buf, int n0,
                                            int row0, int N) {
@@ -201,21 +210,23 @@ __device__ __forceinline__ void store_rows(const CUtensorMap& map, const float (
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                       reinterpret_cast<uint64_t>(&map)),
-                   "r"(n0 + c), "r"(row0), "r"(buf)
-                   : "memory");
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
+    if (lane == 0) store_box(map, n0 + c, row0, buf);
   }
 }
 
-template <int CG, int BN>
+// What becomes of a tile: rows of the output, or (kGateUp) SiLU(gate) * up quantised to FP8. A
+// kGateUp tile holds 128 gate columns and the 128 up columns of the same intermediate ones
+// (rank 0 of the pair loads the former's weight rows, rank 1 the latter's); a promotion
+// thread takes 64 of each, so the product needs no exchange, and the block's maximum one of
+// a word per row between two warps.
+enum Epilogue { kRows = 0, kGateUp = 1 };
+
+template <int CG, int BN, int EPI>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fp8_tile_kernel(const __grid_constant__ TileMaps maps, const Fp8Args p) {
   using Cfg = TileCfg<CG, BN>;
   constexpr int S = Cfg::kStages, COLS = Cfg::kCols;
+  static_assert(EPI == kRows || (CG == 2 && BN == 256), "the gate_up tile");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
@@ -225,6 +236,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* acc_empty = acc_full + 2;                  // [2] buffer read by every warp (rank 0's is used)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   __shared__ int abort_flag;
+  // kGateUp: maxima of the rows by column half, in the half of a staging box it does not use
+  uint32_t(*row_max)[kBM] =
+      reinterpret_cast<uint32_t(*)[kBM]>(smem + kFixedBytes + S * Cfg::kStageBytes + kStagingBytes / 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
@@ -250,6 +264,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile int* abort_v = &abort_flag;
 
   const int KB = fp8_blocks(p.K), NT = (p.N + BN - 1) / BN, NB = fp8_blocks(p.N);
+  const int I = p.N / 2;  // kGateUp
   // 32 bits: the host checks that the tiles' number fits
   const int units = p.layout == kFp8Dense ? int((p.rows + kBM * CG - 1) / (kBM * CG)) : p.ntp[0] / (kBM * CG);
   const int tiles = units * NT;
@@ -270,6 +285,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int u = t / NT, nt = t - u * NT;
           int row;
           if (of_x) row = (p.layout == kFp8Dense ? u * kBM * CG : __ldg(p.block_row0 + u)) + int(rank) * kBM;
+          else if (EPI == kGateUp) row = int(rank) * I + nt * kFp8Block;
           else row = (p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u)) * p.N + nt * BN + int(rank) * Cfg::kBRows;
           for (int kb = 0; kb < KB; ++kb, ++fill) {
             const uint32_t s = fill % S;
@@ -324,13 +340,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int h = (warp - kFirstPromoteWarp) >> 2;     // its half of the columns
     const int r = q * 32 + lane;
     const uint32_t empty0 = CG == 2 ? cluster_addr(acc_empty, 0) : smem_u32(acc_empty);
-    const uint32_t src = tmem + (uint32_t(q * 32) << 16) + h * COLS;
+    const uint32_t src = tmem + (uint32_t(q * 32) << 16) + (EPI == kGateUp ? h * 64 : h * COLS);
+    // column (from src) of chunk c: a kGateUp warp's second half are the up columns
+    auto chunk = [](int c) { return EPI == kGateUp && c >= 64 / kChunkCols ? 128 + kChunkCols * c - 64 : kChunkCols * c; };
     const uint32_t staging = sbase + kFixedBytes + S * Cfg::kStageBytes + (warp - kFirstPromoteWarp) * kStagingBytes;
     uint32_t it = 0;
     bool ok = true;
-    for (int t = cid; t < tiles && ok; t += ncl) {
+    // a kGateUp warp that gave up still meets its partner's barriers (its waits return at once)
+    for (int t = cid; t < tiles && (ok || EPI == kGateUp); t += ncl) {
       const int u = t / NT;
-      const int n0 = (t - u * NT) * BN + h * COLS;
+      const int n0 = EPI == kGateUp ? (t - u * NT) * kFp8Block + h * 64 : (t - u * NT) * BN + h * COLS;
       const int e = p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u);
       const int pos = u * kBM * CG + int(rank) * kBM + r;
       const int64_t row = p.layout == kFp8Dense ? pos : __ldg(p.block_row0 + u) + int(rank) * kBM + r;
@@ -339,15 +358,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const float* xs = p.xs + (row < p.rows ? row : 0);
       const int nb = min(n0 / kFp8Block, NB - 1);
       const float* ws = p.ws + (int64_t(e) * NB + nb) * KB;
+      const float* wu = EPI == kGateUp ? ws + int64_t(I / kFp8Block) * KB : ws;  // of the up columns
       uint64_t sum[COLS / 2];  // columns 2i, 2i + 1
 #pragma unroll
       for (int c = 0; c < COLS / 2; ++c) sum[c] = 0;
       // the scales of this k block and the next two (loads run two blocks ahead)
       float x0 = __ldg(xs), w0 = __ldg(ws), x1 = 0.f, w1 = 0.f;
+      float u0 = EPI == kGateUp ? __ldg(wu) : 0.f, u1 = 0.f;
       if (KB > 1) {
         xs += p.rows;
         x1 = __ldg(xs);
         w1 = __ldg(ws + 1);
+        if (EPI == kGateUp) u1 = __ldg(wu + 1);
       }
       // the tensor-memory loads run one chunk of columns ahead of the additions, across k
       // blocks too
@@ -358,14 +380,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tmem_ld_async(src + (it & 1) * BN, v[0]);
 #pragma unroll 1
       for (int kb = 0; kb < KB; ++kb) {
-        const float scale = x0 * w0;
-        const uint64_t s = pack2(scale, scale);
+        const uint64_t s = pack2(x0 * w0, x0 * w0), s_up = EPI == kGateUp ? pack2(x0 * u0, x0 * u0) : s;
         x0 = x1;
         w0 = w1;
+        u0 = u1;
         if (kb + 2 < KB) {
           xs += p.rows;
           x1 = __ldg(xs);
           w1 = __ldg(ws + kb + 2);
+          if (EPI == kGateUp) u1 = __ldg(wu + kb + 2);
         }
         const uint32_t b = it & 1;
         ++it;
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int c = 0; c < CH; ++c) {
           tmem_wait_ld(v[c & 1]);
           if (c + 1 < CH) {
-            tmem_ld_async(src + b * BN + W * (c + 1), v[(c + 1) & 1]);
+            tmem_ld_async(src + b * BN + chunk(c + 1), v[(c + 1) & 1]);
           } else {  // the buffer is read: hand it back, and request the next one's first chunk
             tc_fence_before();
             __syncwarp();
@@ -387,15 +410,49 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_ld_async(src + (it & 1) * BN, v[0]);
           }
 #pragma unroll
-          for (int j = 0; j < W; j += 2) fma2(sum[(W * c + j) / 2], v[c & 1][j], v[c & 1][j + 1], s);
+          for (int j = 0; j < W; j += 2)
+            fma2(sum[(W * c + j) / 2], v[c & 1][j], v[c & 1][j + 1], W * c >= COLS / 2 ? s_up : s);
         }
         if (!ok) break;
       }
       tmem_wait_ld(v[0]);
-      if (!ok) continue;
+      if (!ok && EPI != kGateUp) continue;
       float acc[COLS];
 #pragma unroll
       for (int c = 0; c < COLS / 2; ++c) unpack2(sum[c], acc[2 * c], acc[2 * c + 1]);
+      if (EPI == kGateUp) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          acc[c] = silu_times(acc[c], acc[c + 64]);
+          m = max(m, abs_bits(acc[c]));
+        }
+        row_max[h][r] = m;
+        named_bar_sync(1 + q, 64);  // the two warps of these rows
+        m = max(m, row_max[h ^ 1][r]);
+        named_bar_sync(1 + q, 64);  // both have read before the next tile's maxima
+        float scale, inv;
+        block_scale(m, &scale, &inv);
+        if (ok && row < p.rows && h == 0) p.out_scales[int64_t(n0 / kFp8Block) * p.rows + row] = scale;
+        const int row0 = int(row) - lane;
+        if (!ok || row0 >= p.rows) continue;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 64-byte rows, 64-byte swizzle
+          uint32_t code[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 16 * j + 4 * i;
+            code[i] = e4m3x4(acc[c] * inv, acc[c + 1] * inv, acc[c + 2] * inv, acc[c + 3] * inv);
+          }
+          sts128(staging + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), code);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) store_box(maps.out, n0, row0, staging);
+        continue;
+      }
       // 32 whole rows leave through shared memory by TMA, 128 bytes wide, while the next tile
       // runs (stores of a row per lane held the promotion for about 4 us a tile); rows past a
       // dense matrix are cut off by the copy. Where some rows are not to be written, each lane
@@ -451,26 +508,26 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// A row-major matrix [rows, cols] of `size`-byte elements, boxes of 128 bytes x box_rows rows
-// (128-byte swizzle); what lies outside reads as zero and is not written.
+// A row-major matrix [rows, cols] of `size`-byte elements, boxes of box_bytes (128 or 64, the
+// swizzle too) x box_rows rows; what lies outside reads as zero and is not written.
 cudaError_t matrix_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t rows, int cols,
-                       int box_rows) {
+                       int box_rows, int box_bytes = 128) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
   const cuuint64_t strides[1] = {cuuint64_t(cols) * size};
-  const cuuint32_t box[2] = {cuuint32_t(128 / size), cuuint32_t(box_rows)}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {cuuint32_t(box_bytes / size), cuuint32_t(box_rows)}, one[2] = {1, 1};
   return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
 
-template <int CG, int BN>
+template <int CG, int BN, int EPI>
 cudaError_t launch(const Fp8Args& a, cudaStream_t stream) {
   using Cfg = TileCfg<CG, BN>;
-  auto kern = fp8_tile_kernel<CG, BN>;
+  auto kern = fp8_tile_kernel<CG, BN, EPI>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -505,7 +562,8 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t stream) {
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if ((err = matrix_map(&maps.x, u8, 1, a.xq, a.rows, a.K, kBM)) != cudaSuccess) return err;
   if ((err = matrix_map(&maps.w, u8, 1, a.w, int64_t(a.E) * a.N, a.K, Cfg::kBRows)) != cudaSuccess) return err;
-  err = matrix_map(&maps.out, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+  if (EPI == kGateUp) err = matrix_map(&maps.out, u8, 1, a.out, a.rows, a.N / 2, 32, 64);
+  else err = matrix_map(&maps.out, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                    a.out_f32 ? 4 : 2, a.out, a.rows, a.N, 32);
   if (err != cudaSuccess) return err;
   // upper bound of the tiles (the grouped unit count is on the device)
@@ -521,7 +579,11 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream) {
-  return a.bm == 256 ? launch<2, 256>(a, stream) : launch<1, 128>(a, stream);
+  return a.bm == 256 ? launch<2, 256, kRows>(a, stream) : launch<1, 128, kRows>(a, stream);
+}
+
+cudaError_t launch_fp8_tile_gate_up(const Fp8Args& a, cudaStream_t stream) {
+  return launch<2, 256, kGateUp>(a, stream);
 }
 
 }  // namespace chord
