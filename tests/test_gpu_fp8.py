@@ -171,6 +171,7 @@ DENSE = [
     (1, 8, 16), (1, 128, 128), (1, 4096, 7168), (3, 72, 144), (8, 136, 256), (9, 264, 400), (17, 24, 1024),
     (32, 512, 272), (33, 576, 1520), (64, 136, 2048), (100, 256, 128), (128, 264, 384), (129, 256, 640),
     (255, 520, 272), (300, 1032, 512), (513, 264, 896),
+    (40, 128, 7168), (65, 384, 1040), (120, 136, 4096), (2, 24, 144),
 ]
 
 

@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libchord.so")
 SOURCES = ["api.cu", "align.cu", "align_static.cu", "router.cu", "fp8_api.cu", "fp8_quant.cu", "fp8_stream.cu", "fp8_tile.cu", "repack.cu", "stream_gemm.cu", "stream_gemm_short.cu", "tc_gemm.cu", "permute.cu", "grouped.cu", "shard.cu",
            "combine.cu", "diag.cu"]
-HEADERS = ["chord_internal.cuh", "align_common.cuh", "fp8.cuh", "tc_common.cuh", "stream_common.cuh"]
+HEADERS = ["chord_internal.cuh", "align_common.cuh", "fp8.cuh", "fp8_tc.cuh", "tc_common.cuh", "stream_common.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

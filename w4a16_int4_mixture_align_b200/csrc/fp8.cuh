@@ -11,7 +11,7 @@ constexpr float kFp8Max = 448.f;
 __host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
 
 // Workspace of the products: the zero-once header, then the unit lists of the grouped
-// layouts (units of 8 to 256 rows, written by the routing pass).
+// layouts (units of 16 to 256 rows, written by the routing pass).
 struct Fp8Workspace {
   int64_t max_positions, ntp_offset, expert_ids_offset, block_row0_offset, sorted_ids_offset, total;
 };
@@ -76,8 +76,8 @@ __device__ __forceinline__ float silu_times(float g, float u) { return __fdiv_rn
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t stream);
-// Any number of rows; a.bm in {8, 16, 32}.
-cudaError_t launch_fp8_stream(const Fp8Args& a, cudaStream_t stream);
+// a.bm in {16, 32, 64, 128}; likely_units: units of bm rows the caller expects (performance only).
+cudaError_t launch_fp8_stream(const Fp8Args& a, int64_t likely_units, cudaStream_t stream);
 // a.bm in {128, 256}: single CTAs or CTA pairs.
 cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream);
 // Dense, w = [gate; up] with a.N = 2 I: SiLU(gate) * up quantised to q [rows, I], scales [I/128, rows].

@@ -73,8 +73,11 @@ Fp8Args product_args(const uint8_t* xq, const float* xs, int64_t rows, int K, co
 // The schedule for `expected` rows per expert, then the product.
 chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices, const int32_t* masked_m,
                            int64_t max_m, void* workspace, int flags, cudaStream_t stream) {
-  const bool tensor = (flags & CHORD_FLAG_FORCE_TENSOR) || (!(flags & CHORD_FLAG_FORCE_STREAM) && expected > 32);
-  a.bm = tensor ? (expected > 128 ? 256 : 128) : (expected <= 8 ? 8 : expected <= 16 ? 16 : 32);
+  const bool tensor = (flags & CHORD_FLAG_FORCE_TENSOR) || (!(flags & CHORD_FLAG_FORCE_STREAM) && expected > 128);
+  if (tensor) a.bm = expected > 128 ? 256 : 128;
+  else if (a.layout == kFp8Dense) a.bm = expected <= 16 ? 16 : expected <= 32 ? 32 : expected <= 64 ? 64 : 128;
+  else a.bm = expected <= 9 ? 16 : expected <= 20 ? 32 : expected <= 44 ? 64 : 128;  // experts above the mean fit too
+  const int64_t likely_units = a.layout == kFp8Dense ? (a.rows + a.bm - 1) / a.bm : a.E * ((expected + a.bm - 1) / a.bm);
   cudaError_t err;
   if (a.layout != kFp8Dense) {
     const Fp8Workspace ws = fp8_workspace(a.rows, a.E);
@@ -91,7 +94,7 @@ chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices
     a.block_row0 = block_row0;
     a.sorted_ids = sorted_ids;
   }
-  err = tensor ? launch_fp8_tile(a, stream) : launch_fp8_stream(a, stream);
+  err = tensor ? launch_fp8_tile(a, stream) : launch_fp8_stream(a, likely_units, stream);
   return err == cudaSuccess ? CHORD_OK : cuda_fail(err, tensor ? "FP8 tensor-core GEMM launch" : "FP8 streaming GEMM launch");
 }
 

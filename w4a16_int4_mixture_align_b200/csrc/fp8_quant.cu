@@ -39,6 +39,8 @@ __device__ __forceinline__ void load8(const void* base, int dtype, int64_t at, f
 
 template <int DTYPE, bool SILU>
 __global__ void __launch_bounds__(32 * kQuantWarps) fp8_quantize_kernel(const Fp8QuantArgs a) {
+  grid_dep_wait();
+  grid_dep_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (a.K + kChunk - 1) / kChunk;
   const int64_t groups = (a.rows + kQuantWarps - 1) / kQuantWarps;
@@ -97,9 +99,10 @@ template <int DTYPE, bool SILU>
 cudaError_t launch(const Fp8QuantArgs& a, cudaStream_t stream) {
   const int64_t items = (a.rows + kQuantWarps - 1) / kQuantWarps * ((a.K + kChunk - 1) / kChunk);
   const int64_t most = int64_t(a.num_sms) * 8;
-  fp8_quantize_kernel<DTYPE, SILU><<<unsigned(items < most ? items : most), 32 * kQuantWarps, 0, stream>>>(a);
+  const cudaError_t err = launch_pdl(true, fp8_quantize_kernel<DTYPE, SILU>, dim3(unsigned(items < most ? items : most)),
+                                     dim3(32 * kQuantWarps), 0, stream, a);
   count_launches(1);
-  return cudaGetLastError();
+  return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace

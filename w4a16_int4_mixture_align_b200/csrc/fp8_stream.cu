@@ -1,156 +1,355 @@
-// fp8_stream.cu -- FP8 block-128 products for few rows: the weights stream through once.
+// fp8_stream.cu -- FP8 block-128 products for up to 128 rows of an expert: the weights stream
+// through once.
 //
-// out[m, n] = sum_kb xs[kb, m] * ws[n/128, kb] * (xq[m, kb] . w[n, kb])
+//   out[m, n] = sum_kb s[m, kb] * P_kb[n, m],   P_kb = w[n, kb] . xq[m, kb],
+//   s = xs[kb, m] * ws[n/128, kb]
 //
-// With a handful of rows the product reads N*K weight bytes for 2*N*K*rows operations, so
-// HBM bounds it. A CTA owns 16 weight rows of one unit (up to 8, 16 or 32 activation rows);
-// its eight warps share out the 128-wide k blocks, so a CTA streams 8 x 2 KiB at a time.
-// Weights go straight from global memory to mma.m16n8k32 fragments (weight rows in the M
-// slot, activation rows in N): a dot product does not care in which order its k are
-// numbered, so lane (g, t) takes the 16 contiguous bytes at 16t of each 64-byte half of its
-// rows, for weights and activations alike, and every load is a full 16 bytes.
-// The four products of a block start from zero, and their sum joins the FP32 accumulator
-// through one fused multiply-add with xs * ws. The warps' accumulators meet in shared
-// memory and are added in warp order.
-#include "fp8.cuh"
+// With few rows the product reads N*K weight bytes for 2*N*K*rows operations, so HBM bounds
+// it. The operands are swapped against fp8_tile.cu: a tile of 128 weight rows (one block of
+// the weight scales) is the M side of the MMA and TN = 16 to 128 activation rows the N side,
+// so a weight byte is fetched once for all of them and the MMA's size follows the rows.
+//
+//   warp 0      TMA producer: per k block 128 weight rows and TN activation rows, 128 bytes
+//               wide (128-byte swizzle), into a ring of stages.
+//   warp 1      MMA issuer: four tcgen05.mma (M = 128, N = TN, K = 32) into one of several
+//               tensor-memory buffers.
+//   warp 2      scales: s of eight k blocks at a time into a ring in shared memory.
+//   warps 4..7  promotion: one weight row per thread, TN columns; FP32 accumulation in
+//               registers, s read as broadcast vectors.
+//
+// An item is (unit of TN rows, weight tile). With many items a CTA runs them one after
+// another. With few (one token against a 4096 x 7168 matrix has 32) a cluster of S CTAs
+// shares an item, each taking 1/S of the k blocks; their FP32 sums meet through distributed
+// shared memory, are added in rank order, and each CTA writes its share of the rows.
+//
+// All waits are bounded; on a timeout the CTA raises CHORD_DEV_TIMEOUT, writes nothing more,
+// waits (bounded) for what it has in flight and returns.
+#include <mutex>
+
+#include "fp8_tc.cuh"
 
 namespace chord {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kRows = 16;  // weight rows of a CTA item
+constexpr int kWRows = 128;                     // weight rows of a tile
+constexpr int kWBytes = kWRows * kFp8Block;
+constexpr int kThreads = 256;
+constexpr int kFirstPromote = 4, kPromote = 4;  // warps
+constexpr int kGroupKb = 8;                     // k blocks of a scale group
 
-__device__ __forceinline__ void mma_e4m3_16832(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+template <int TN>
+struct StreamCfg {
+  // TN <= 64: two CTAs share an SM (half the shared memory and tensor memory, 128 registers
+  // a thread), so one's start and end overlap the other's streaming
+  static constexpr int kCtas = TN <= 64 ? 2 : 1;
+  static constexpr int kStageBytes = kWBytes + TN * kFp8Block;
+  static constexpr int kGroups = 3;                               // scale groups in the ring
+  static constexpr int kScaleBytes = kGroups * kGroupKb * TN * 4;
+  static constexpr int kFixed = 1024 + kScaleBytes;
+  static constexpr int kBudget = (TN <= 64 ? 113 : 226) * 1024 - 1024;  // less alignment slack
+  static constexpr int kStages = (kBudget - kFixed) / kStageBytes;
+  static constexpr int kSmem = 1024 + (kFixed + 1023) / 1024 * 1024 + kStages * kStageBytes;
+  static constexpr int kBufs = 4;
+  static constexpr int kCols = kBufs * TN;                        // 64 .. 512, a power of two
+  static constexpr int kChunk = 16;
+};
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+struct StreamMaps {
+  CUtensorMap x, w;
+};
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 
-template <int NT>
-struct Frag {
-  uint4 a[2][2];   // [row g, g + 8][64-byte half]
-  uint4 b[NT][2];  // [activation rows 8 nt + g][half]
-  float s[NT][2];  // scales of activation rows 8 nt + 2t, + 1, times the weight scale
-};
+template <int TN>
+__global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
+    fp8_stream_kernel(const __grid_constant__ StreamMaps maps, const Fp8Args p, int split) {
+  using Cfg = StreamCfg<TN>;
+  constexpr int S = Cfg::kStages, B = Cfg::kBufs, W = Cfg::kChunk;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [S]
+  uint64_t* empty = full + S;                          // [S]
+  uint64_t* acc_full = empty + S;                      // [B]
+  uint64_t* acc_empty = acc_full + B;                  // [B]
+  uint64_t* sc_full = acc_empty + B;                   // [kGroups]
+  uint64_t* sc_empty = sc_full + Cfg::kGroups;         // [kGroups]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_empty + Cfg::kGroups);
+  float* scales = reinterpret_cast<float*>(smem + 1024);  // [kGroups][kGroupKb][TN]
+  uint8_t* ring = smem + (Cfg::kFixed + 1023) / 1024 * 1024;
+  float* partial = reinterpret_cast<float*>(ring);        // [TN][128], once the ring is spent
+  __shared__ int abort_flag;
 
-template <int NT>
-__global__ void __launch_bounds__(32 * kWarps) fp8_stream_kernel(const Fp8Args p) {
-  constexpr int TC = 8 * NT;
-  __shared__ float red[kWarps][TC][kRows + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int KB = fp8_blocks(p.K), NB = fp8_blocks(p.N);
-  const int tiles = (p.N + kRows - 1) / kRows;
-  const int64_t units = p.layout == kFp8Dense ? (p.rows + TC - 1) / TC : p.ntp[0] / TC;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-
-  for (int64_t item = blockIdx.x; item < units * tiles; item += gridDim.x) {
-    const int64_t u = item / tiles;
-    const int n0 = int(item - u * tiles) * kRows;
-    const int e = p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u);
-    auto row_of = [&](int j) -> int64_t {  // activation row of the unit's position j, or -1
-      if (p.layout == kFp8Dense) return u * TC + j < p.rows ? u * TC + j : -1;
-      return __ldg(p.sorted_ids + u * TC + j);
-    };
-    int64_t rb[NT], rs[NT][2];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      rb[i] = row_of(8 * i + g);
-      rs[i][0] = row_of(8 * i + 2 * t);
-      rs[i][1] = row_of(8 * i + 2 * t + 1);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    // rows past N repeat the last one; they are not stored
-    const uint8_t* w0 = p.w + (int64_t(e) * p.N + min(n0 + g, p.N - 1)) * p.K;
-    const uint8_t* w1 = p.w + (int64_t(e) * p.N + min(n0 + g + 8, p.N - 1)) * p.K;
-    const float* ws = p.ws + (int64_t(e) * NB + n0 / kFp8Block) * KB;
+    for (int b = 0; b < B; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kPromote);
+    }
+    for (int g = 0; g < Cfg::kGroups; ++g) {
+      mbar_init(&sc_full[g], 32);
+      mbar_init(&sc_empty[g], kPromote);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc<1>(tmem_slot, Cfg::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  volatile int* abort_v = &abort_flag;
+  grid_dep_wait();
+  grid_dep_trigger();
 
-    auto load = [&](int kb, Frag<NT>& f) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = kb * kFp8Block + 64 * h + 16 * t;  // K % 16 == 0: a vector is all in or all out
-        const bool in = k < p.K;
-        f.a[0][h] = in ? ldg_stream(w0 + k) : zero;
-        f.a[1][h] = in ? ldg_stream(w1 + k) : zero;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          f.b[i][h] = in && rb[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.xq + rb[i] * p.K + k)) : zero;
-      }
-      const float sw = __ldg(ws + kb);
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) f.s[i][j] = rs[i][j] >= 0 ? __ldg(p.xs + kb * p.rows + rs[i][j]) * sw : 0.f;
-    };
+  const uint32_t rank = split > 1 ? cluster_rank() : 0;
+  const int KB = fp8_blocks(p.K), NT = (p.N + kWRows - 1) / kWRows;
+  const int kb_begin = int(rank) * KB / split, kb_end = (int(rank) + 1) * KB / split;
+  const int units = p.layout == kFp8Dense ? int((p.rows + TN - 1) / TN) : p.ntp[0] / TN;
+  const int items = units * NT;
+  const int first = split > 1 ? int(cluster_id_x()) : int(blockIdx.x);
+  const int step = split > 1 ? int(num_clusters_x()) : int(gridDim.x);  // a split grid covers all items
+  auto unit_row0 = [&](int u) { return p.layout == kFp8Dense ? u * TN : __ldg(p.block_row0 + u); };
+  auto unit_expert = [&](int u) { return p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u); };
 
-    float acc[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    Frag<NT> cur, nxt;
-    if (warp < KB) load(warp, cur);
-    for (int kb = warp; kb < KB; kb += kWarps) {
-      if (kb + kWarps < KB) load(kb + kWarps, nxt);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mma_e4m3_16832(c, cur.a[0][h].x, cur.a[1][h].x, cur.a[0][h].y, cur.a[1][h].y, cur.b[i][h].x, cur.b[i][h].y);
-          mma_e4m3_16832(c, cur.a[0][h].z, cur.a[1][h].z, cur.a[0][h].w, cur.a[1][h].w, cur.b[i][h].z, cur.b[i][h].w);
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t fill = 0;
+      bool ok = true;
+      for (int i = first; i < items && ok; i += step) {
+        const int u = i / NT, row = unit_row0(u), wrow = unit_expert(u) * p.N + (i - u * NT) * kWRows;
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++fill) {
+          const uint32_t s = fill % S;
+          if (fill >= S && !mbar_wait(&empty[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+          const uint32_t st = smem_u32(ring + s * Cfg::kStageBytes);
+          tma_2d<1>(st, &maps.w, kb * kFp8Block, wrow, smem_u32(&full[s]));
+          tma_2d<1>(st + kWBytes, &maps.x, kb * kFp8Block, row, smem_u32(&full[s]));
         }
-        acc[i][0] = fmaf(c[0], cur.s[i][0], acc[i][0]);
-        acc[i][1] = fmaf(c[1], cur.s[i][1], acc[i][1]);
-        acc[i][2] = fmaf(c[2], cur.s[i][0], acc[i][2]);
-        acc[i][3] = fmaf(c[3], cur.s[i][1], acc[i][3]);
       }
-      cur = nxt;
+      int dummy = 0;  // the last copies have landed before the CTA ends
+      for (uint32_t f = fill > S ? fill - S : 0; f < fill; ++f) mbar_wait(&full[f % S], (f / S) & 1, &dummy, p.status);
     }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(kWRows, TN);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = first; i < items && ok; i += step) {
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++it) {
+          const uint32_t s = it % S, b = it % B;
+          if ((it >= B && !mbar_wait(&acc_empty[b], ((it / B) - 1) & 1, abort_v, p.status)) ||
+              !mbar_wait(&full[s], (it / S) & 1, abort_v, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_u32(ring + s * Cfg::kStageBytes);
+          const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kWBytes);
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+          for (int k = 0; k < 4; ++k) mma_e4m3<1>(tmem + b * TN, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+          commit<1>(&empty[s]);
+          commit<1>(&acc_full[b]);
+        }
+      }
+      if (it > 0) {  // no MMA writes tensor memory once it is freed
+        int dummy = 0;
+        mbar_wait(&empty[(it - 1) % S], ((it - 1) / S) & 1, &dummy, p.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    uint32_t grp = 0;
+    bool ok = true;
+    for (int i = first; i < items && ok; i += step) {
+      const int u = i / NT, nb = i - u * NT;
+      const int64_t row0 = unit_row0(u);
+      const float* ws = p.ws + (int64_t(unit_expert(u)) * NT + nb) * KB;  // NT = the weight scales' row blocks
+      for (int kb0 = kb_begin; kb0 < kb_end; kb0 += kGroupKb, ++grp) {
+        const uint32_t g = grp % Cfg::kGroups;
+        constexpr int PER = kGroupKb * TN / 32;
+        float v[PER];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) red[warp][8 * i + 2 * t + (j & 1)][g + 8 * (j >> 1)] = acc[i][j];
+        for (int j = 0; j < PER; ++j) {
+          const int at = 32 * j + lane, kb = kb0 + at / TN;
+          const int64_t row = row0 + at % TN;
+          // rows and blocks that do not exist are never used
+          v[j] = kb < kb_end && row < p.rows ? __ldg(p.xs + kb * p.rows + row) * __ldg(ws + kb) : 0.f;
+        }
+        if (grp >= Cfg::kGroups && !mbar_wait_warp(&sc_empty[g], ((grp / Cfg::kGroups) - 1) & 1, abort_v, p.status)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) scales[g * kGroupKb * TN + 32 * j + lane] = v[j];
+        mbar_arrive(&sc_full[g]);
+      }
+    }
+  } else if (warp >= kFirstPromote) {
+    const int q = warp & 3;  // the tensor-memory lanes this warp may read
+    const int r = q * 32 + lane;
+    const uint32_t src = tmem + (uint32_t(q * 32) << 16);
+    uint32_t it = 0, grp = 0;
+    bool ok = true;
+    for (int i = first; i < items && ok; i += step) {
+      const int u = i / NT, n = (i - u * NT) * kWRows + r;
+      uint64_t sum[TN / 2];  // columns 2j, 2j + 1
+#pragma unroll
+      for (int j = 0; j < TN / 2; ++j) sum[j] = 0;
+      for (int kb = kb_begin; kb < kb_end; ++kb, ++it) {
+        const uint32_t g = grp % Cfg::kGroups;
+        const int in_group = (kb - kb_begin) % kGroupKb;
+        if (in_group == 0) ok = mbar_wait_warp(&sc_full[g], (grp / Cfg::kGroups) & 1, abort_v, p.status);
+        const uint32_t b = it % B;
+        ok = ok && mbar_wait_warp(&acc_full[b], (it / B) & 1, abort_v, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sc = smem_u32(scales + (g * kGroupKb + in_group) * TN);
+        uint32_t v[2][W];
+        tmem_ld_async(src + b * TN, v[0]);
+#pragma unroll
+        for (int c = 0; c < TN / W; ++c) {
+          tmem_wait_ld(v[c & 1]);
+          if (c + 1 < TN / W) {
+            tmem_ld_async(src + b * TN + W * (c + 1), v[(c + 1) & 1]);
+          } else {  // the buffer is read: hand it back
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < W; j += 4) {
+            const uint4 s4 = lds128(sc + (W * c + j) * 4);
+            fma2(sum[(W * c + j) / 2], v[c & 1][j], v[c & 1][j + 1], (uint64_t(s4.y) << 32) | s4.x);
+            fma2(sum[(W * c + j) / 2 + 1], v[c & 1][j + 2], v[c & 1][j + 3], (uint64_t(s4.w) << 32) | s4.z);
+          }
+        }
+        if (in_group == kGroupKb - 1 || kb == kb_end - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_empty[g]);
+          ++grp;
+        }
+      }
+      if (!ok) break;
+      if (split > 1) {
+#pragma unroll
+        for (int j = 0; j < TN / 2; ++j) {
+          float lo, hi;
+          unpack2(sum[j], lo, hi);
+          partial[(2 * j) * kWRows + r] = lo;
+          partial[(2 * j + 1) * kWRows + r] = hi;
+        }
+        continue;
+      }
+      // a row of the output at a time: 32 neighbouring columns a warp
+      const int row0 = unit_row0(u);
+#pragma unroll
+      for (int j0 = 0; j0 < TN; j0 += 32) {
+        const int j = j0 + lane;
+        const bool mine = j < TN && (p.layout == kFp8Dense ? row0 + j < p.rows : __ldg(p.sorted_ids + u * TN + j) >= 0);
+        const uint32_t live = __ballot_sync(0xffffffffu, mine);
+        if (n >= p.N) continue;
+#pragma unroll
+        for (int k = 0; k < 32 && j0 + k < TN; ++k) {
+          if (!((live >> k) & 1u)) continue;
+          float lo, hi;
+          unpack2(sum[(j0 + k) / 2], lo, hi);
+          const float x = (k & 1) ? hi : lo;
+          const int64_t at = int64_t(row0 + j0 + k) * p.N + n;
+          if (p.out_f32) static_cast<float*>(p.out)[at] = x;
+          else static_cast<uint16_t*>(p.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) {
+    cluster_sync_all();  // every CTA's sums are in its shared memory
+    const int j_begin = int(rank) * TN / split, j_end = (int(rank) + 1) * TN / split;
+    if (first < items && !abort_flag) {
+      const int u = first / NT, n0 = (first - u * NT) * kWRows, row0 = unit_row0(u);
+      for (int i = threadIdx.x; i < (j_end - j_begin) * kWRows; i += kThreads) {
+        const int j = j_begin + i / kWRows, n = n0 + i % kWRows;
+        const bool live = p.layout == kFp8Dense ? row0 + j < p.rows : __ldg(p.sorted_ids + u * TN + j) >= 0;
+        if (!live || n >= p.N) continue;
+        const float* mine = partial + j * kWRows + i % kWRows;
+        float x = 0.f;
+        for (int c = 0; c < split; ++c) x += ld_cluster(cluster_addr(mine, c));
+        const int64_t at = int64_t(row0 + j) * p.N + n;
+        if (p.out_f32) static_cast<float*>(p.out)[at] = x;
+        else static_cast<uint16_t*>(p.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+      }
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < TC * kRows; i += 32 * kWarps) {
-      const int j = i / kRows, r = i % kRows, n = n0 + r;
-      const int64_t row = row_of(j);
-      if (row < 0 || n >= p.N) continue;
-      float s = red[0][j][r];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) s += red[w][j][r];
-      if (p.out_f32) static_cast<float*>(p.out)[row * p.N + n] = s;
-      else static_cast<uint16_t*>(p.out)[row * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
-    }
-    __syncthreads();  // red is rewritten by the next item
+    cluster_sync_all();  // the sums have been read before their CTA ends
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, Cfg::kCols);
   }
 }
 
-template <int NT>
-cudaError_t launch(const Fp8Args& a, int64_t items, cudaStream_t stream) {
-  const int64_t most = int64_t(a.num_sms) * 4;
-  fp8_stream_kernel<NT><<<unsigned(items < most ? items : most), 32 * kWarps, 0, stream>>>(a);
+template <int TN>
+cudaError_t launch(const Fp8Args& a, int64_t likely_units, cudaStream_t stream) {
+  using Cfg = StreamCfg<TN>;
+  static_assert(Cfg::kStages >= 3 && Cfg::kStages * Cfg::kStageBytes >= TN * kWRows * 4, "ring");
+  auto kern = fp8_stream_kernel<TN>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  if (err != cudaSuccess) return err;
+  StreamMaps maps;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if ((err = matrix_map(&maps.x, u8, 1, a.xq, a.rows, a.K, TN)) != cudaSuccess) return err;
+  if ((err = matrix_map(&maps.w, u8, 1, a.w, int64_t(a.E) * a.N, a.K, kWRows)) != cudaSuccess) return err;
+  const int64_t tiles = (a.N + kWRows - 1) / kWRows, KB = fp8_blocks(a.K);
+  // upper bound of the items (the grouped unit count is on the device)
+  const int64_t items = ((a.rows + TN - 1) / TN + (a.layout == kFp8Dense ? 0 : a.E)) * tiles;
+  if (items >= int64_t(1) << 28) return cudaErrorInvalidValue;
+  // CTAs that share an item: as many as keep the likely items within one wave, each with two
+  // k blocks at least
+  const int64_t slots = int64_t(a.num_sms) * Cfg::kCtas;
+  int split = 1;
+  while (split < 8 && likely_units * tiles * split * 2 <= slots && KB >= 4 * split) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(unsigned(split > 1 ? items * split : (items < slots ? items : slots)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, kern, maps, a, split);
   count_launches(1);
-  return cudaGetLastError();
+  return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_stream(const Fp8Args& a, cudaStream_t stream) {
-  // upper bound of the items (the grouped unit count is on the device)
-  const int64_t units = (a.rows + a.bm - 1) / a.bm + (a.layout == kFp8Dense ? 0 : a.E);
-  const int64_t items = units * ((a.N + kRows - 1) / kRows);
-  if (a.bm == 8) return launch<1>(a, items, stream);
-  if (a.bm == 16) return launch<2>(a, items, stream);
-  return launch<4>(a, items, stream);
+cudaError_t launch_fp8_stream(const Fp8Args& a, int64_t likely_units, cudaStream_t stream) {
+  switch (a.bm) {
+    case 16: return launch<16>(a, likely_units, stream);
+    case 32: return launch<32>(a, likely_units, stream);
+    case 64: return launch<64>(a, likely_units, stream);
+    default: return launch<128>(a, likely_units, stream);
+  }
 }
 
 }  // namespace chord
