@@ -50,6 +50,7 @@ _DTYPES = {torch.float32: CHORD_DTYPE_F32, torch.bfloat16: CHORD_DTYPE_BF16, tor
 
 CHORD_SCORE_SOFTMAX = 0
 CHORD_SCORE_SIGMOID = 1
+_FP8_TYPES = (torch.float8_e4m3fn, torch.uint8)
 _SCORES = {"softmax": CHORD_SCORE_SOFTMAX, "sigmoid": CHORD_SCORE_SIGMOID}
 
 # every symbol include/chord.h declares: (name, restype, argtypes)
@@ -132,20 +133,20 @@ def _ptr(t):
     if t is None:
         return None
     assert t.is_cuda and t.is_contiguous(), "device tensors must be contiguous CUDA tensors"
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _rows_ptr(t):
     """Pointer of a 2-D tensor whose rows are contiguous but may lie apart (a slice of wider
     rows), and the distance between rows in elements."""
     assert t.is_cuda and t.dim() == 2, "expected a 2-D CUDA tensor"
-    if t.shape[0] <= 1 or t.shape[1] == 0:
-        ld = t.shape[1]
-    else:
-        ld = t.stride(0)
-    assert t.shape[1] <= 1 or t.stride(1) == 1, "rows must be contiguous"
-    assert ld >= t.shape[1], "rows must not overlap"
-    return ctypes.c_void_p(t.data_ptr()), ld
+    rows, cols = t.shape
+    step, inner = t.stride()
+    assert cols <= 1 or inner == 1, "rows must be contiguous"
+    if rows <= 1 or cols == 0:
+        return t.data_ptr(), cols
+    assert step >= cols, "rows must not overlap"
+    return t.data_ptr(), step
 
 
 def _typed(t, dtype, what, numel=None):
@@ -156,8 +157,10 @@ def _typed(t, dtype, what, numel=None):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: torch.cuda.current_stream() builds an object, which takes 3 us
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _nbytes(t) -> int:
@@ -252,9 +255,9 @@ def chord_router_scored_align(logits, topk, E, block_m, topk_ids, topk_weights, 
     _typed(topk_ids, torch.int32, "topk_ids", T * topk)
     _typed(topk_weights, torch.float32, "topk_weights", T * topk)
     _typed(bias, torch.float32, "bias", G)
-    cap = chord_moe_align_capacity(T, topk, E, block_m)
+    cap = T * topk + E * (block_m - 1)  # chord_moe_align_capacity
     _typed(sorted_ids, torch.int32, "sorted_ids", cap)
-    _typed(expert_ids, torch.int32, "expert_ids", (cap + block_m - 1) // block_m if block_m > 0 else None)
+    _typed(expert_ids, torch.int32, "expert_ids", -(-cap // block_m) if block_m > 0 else None)
     _typed(expert_offsets, torch.int32, "expert_offsets", E + 1)
     ws_bytes = 0 if workspace is None else _nbytes(workspace)
     _check(lib().chord_router_scored_align(ptr, _DTYPES[logits.dtype], ld, _ptr(bias), T, G, topk, E, block_m,
@@ -312,21 +315,23 @@ def chord_grouped_masked(x, masked_m, expected_m, w, N, out, workspace, flags=0,
 # e4m3 [E, N, K] (or [N, K]) with scales fp32 [E, ceil(N/128), ceil(K/128)].
 
 def _fp8_codes(t, what, shape=None):
-    assert t.dtype in (torch.float8_e4m3fn, torch.uint8), f"{what} must hold e4m3 codes, not {t.dtype}"
-    assert shape is None or tuple(t.shape) == tuple(shape), f"{what} has shape {tuple(t.shape)}, needs {tuple(shape)}"
+    assert t.dtype in _FP8_TYPES, f"{what} must hold e4m3 codes, not {t.dtype}"
+    assert shape is None or t.shape == shape, f"{what} has shape {tuple(t.shape)}, needs {shape}"
     return _ptr(t)
 
 
 def _fp8_scales(t, what, shape):
-    _typed(t, torch.float32, what)
-    assert tuple(t.shape) == tuple(shape), f"{what} has shape {tuple(t.shape)}, needs {tuple(shape)}"
+    assert t.dtype == torch.float32, f"{what} must be fp32, not {t.dtype}"
+    assert t.shape == shape, f"{what} has shape {tuple(t.shape)}, needs {shape}"
     return _ptr(t)
 
 
 def _fp8_out(out, rows, N, flags):
-    assert tuple(out.shape) == (rows, N), f"out has shape {tuple(out.shape)}, needs {(rows, N)}"
-    assert out.dtype in (torch.bfloat16, torch.float32), f"out must be bf16 or fp32, not {out.dtype}"
-    return _ptr(out), flags | (CHORD_FLAG_OUTPUT_FP32 if out.dtype == torch.float32 else 0)
+    assert out.shape == (rows, N), f"out has shape {tuple(out.shape)}, needs {(rows, N)}"
+    if out.dtype == torch.float32:
+        return _ptr(out), flags | CHORD_FLAG_OUTPUT_FP32
+    assert out.dtype == torch.bfloat16, f"out must be bf16 or fp32, not {out.dtype}"
+    return _ptr(out), flags
 
 
 def _blocks128(n) -> int:
@@ -345,7 +350,7 @@ def _fp8_quantize(name, x, q, scales, masked_m, width, stream):
     x2 = x.flatten(0, 1) if x.dim() == 3 else x  # [E, max_m, K] of the masked layout
     q2 = q.flatten(0, 1) if q.dim() == 3 else q
     rows, K = q2.shape
-    assert tuple(x2.shape) == (rows, width * K), f"input has shape {tuple(x2.shape)}, codes {tuple(q2.shape)}"
+    assert x2.shape == (rows, width * K), f"input has shape {tuple(x2.shape)}, codes {tuple(q2.shape)}"
     assert x.dtype in (torch.bfloat16, torch.float32), f"input must be bf16 or fp32, not {x.dtype}"
     ptr, ld = _rows_ptr(x2)
     _typed(masked_m, torch.int32, "masked_m")
@@ -609,6 +614,7 @@ class ChordFP8MLP:
         need = max(chord_fp8_gate_up_workspace_bytes(T, self.I), chord_fp8_workspace_bytes(T, 1))
         self.workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=d)
         self.max_tokens = T
+        self.viewed, self.views = -1, None
 
     def forward(self, x, out=None, flags=0):
         """out [T, H] (bf16, or the fp32 sums if an fp32 `out` is given) for bf16 or fp32 x [T, H]."""
@@ -619,8 +625,11 @@ class ChordFP8MLP:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         if T == 0:
             return out
-        xq, xs = self.xq[:T * self.H].view(T, self.H), self.xs[:T * _blocks128(self.H)].view(-1, T)
-        aq, a_s = self.aq[:T * self.I].view(T, self.I), self.as_[:T * _blocks128(self.I)].view(-1, T)
+        if T != self.viewed:  # the buffers seen as T rows
+            self.views = (self.xq[:T * self.H].view(T, self.H), self.xs[:T * _blocks128(self.H)].view(-1, T),
+                          self.aq[:T * self.I].view(T, self.I), self.as_[:T * _blocks128(self.I)].view(-1, T))
+            self.viewed = T
+        xq, xs, aq, a_s = self.views
         chord_fp8_quantize(x, xq, xs)
         chord_fp8_gate_up(xq, xs, self.w13, self.s13, aq, a_s, self.workspace, flags)
         chord_fp8_gemm(aq, a_s, self.w2, self.s2, out, self.workspace, flags)
