@@ -188,7 +188,7 @@ CHORD_API chord_status_t chord_router_topk_align(const float* logits, int64_t T,
  * each row are read. The other arguments, limits and the workspace rule are those of
  * chord_moe_align, plus: topk <= E_global <= 1024, 1 <= n_group <= 32, E_global % n_group
  * == 0, 1 <= topk_group <= n_group, topk <= topk_group * (E_global / n_group), finite scale.
- * Up to 8 tokens run as one launch.
+ * Up to 256 tokens run as one launch.
  * ---------------------------------------------------------------------------------- */
 CHORD_API chord_status_t chord_router_scored_align(
     const void* logits, int logits_dtype, int64_t ld_logits, const float* bias, int64_t T, int E_global, int topk,

@@ -13,6 +13,8 @@
 //
 //   n <= 4 x 1024  : one CTA of 32 warps (runs of ceil(n/1024) steps) does count, scan,
 //                    scatter and fill (1 launch)
+//   n <= 2^18      : a cluster of eight such CTAs, whose counts meet in distributed shared
+//                    memory (1 launch)
 //   larger n       : count kernel (per-chunk histograms) -> scan kernel (1 CTA) ->
 //                    scatter + fill kernel, histograms in the caller's workspace. A chunk
 //                    (one warp's run) is 256 slots, so a prefill batch spreads over
@@ -26,6 +28,8 @@
 namespace chord {
 namespace {
 
+constexpr int kChunk = 1024;       // flat slots per warp chunk (largest)
+constexpr int kSteps = kChunk / 32;
 constexpr int kChunkSmall = 256;   // multi-CTA path, when the histograms stay small
 constexpr int64_t kMaxHistEntries = int64_t(1) << 17;
 
@@ -34,17 +38,126 @@ __host__ __device__ inline int multi_chunk(int64_t n, int E) {
   const int64_t g = (n + kChunkSmall - 1) / kChunkSmall;
   return int64_t(E) * g <= kMaxHistEntries ? kChunkSmall : kChunk;
 }
-// Up to this many 1024-slot chunks the routing sort runs in one CTA (one launch); above
-// it the count / scan / scatter kernels spread the slots over the GPU (one CTA sorting
-// 32 chunks took ~70 us).
+// Up to this many 1024-slot chunks the routing sort runs in one CTA; above it, one cluster
+// sorts up to kClusterMaxSlots slots, and more go to the count / scan / scatter kernels (one
+// CTA sorting 32 chunks took ~70 us).
 constexpr int kSingleMaxChunks = 4;
+constexpr int kSortCtas = 8;
+constexpr int64_t kClusterMaxSlots = int64_t(kSortCtas) * 32 * 32 * 32;  // 32 steps a warp
 
-__global__ void __launch_bounds__(1024) align_single_kernel(
-    const int32_t* __restrict__ ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks,
-    int32_t* __restrict__ sorted_ids, int32_t* __restrict__ expert_ids, int32_t* __restrict__ ntp_out,
-    int32_t* __restrict__ offsets_out) {
+// Loads the ids of `steps` (<= kSteps) 32-slot steps starting at c0, all up front so the
+// loads overlap; slots past n read as -1 (not local).
+__device__ __forceinline__ void load_steps(const int32_t* ids, int64_t n, int64_t c0, int steps,
+                                           int v[kSteps]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int64_t f = c0 + int64_t(s) * 32 + lane;
+    v[s] = (s < steps && f < n) ? __ldg(ids + f) : -1;
+  }
+}
+
+// hist_row[e] += number of local slots of expert e among the loaded steps (warp-cooperative).
+// Non-local slots carry key E.
+__device__ __forceinline__ void chunk_count(const int v[kSteps], int steps, int E, int nbits,
+                                            int* hist_row) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (s >= steps) break;
+    const int e = v[s];
+    const bool loc = is_local(e, E);
+    const unsigned peers = peers_of(loc ? unsigned(e) : unsigned(E), nbits);
+    if (loc && lane == __ffs(peers) - 1) hist_row[e] += __popc(peers);
+    __syncwarp();
+  }
+}
+
+// Places every local slot of the loaded steps at run_row[e] + (rank inside the expert),
+// advancing run_row[e]. Ranks follow increasing flat index.
+__device__ __forceinline__ void chunk_scatter(const int v[kSteps], int steps, int64_t c0, int E,
+                                              int nbits, int* run_row, int32_t* sorted_ids) {
+  const int lane = threadIdx.x & 31;
+  const unsigned lower = (1u << lane) - 1u;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (s >= steps) break;
+    const int e = v[s];
+    const bool loc = is_local(e, E);
+    const unsigned peers = peers_of(loc ? unsigned(e) : unsigned(E), nbits);
+    if (loc) sorted_ids[run_row[e] + __popc(peers & lower)] = int32_t(c0 + int64_t(s) * 32 + lane);
+    __syncwarp();
+    if (loc && lane == __ffs(peers) - 1) run_row[e] += __popc(peers);
+    __syncwarp();
+  }
+}
+
+// Sentinel fill and expert_ids, shared by both paths.
+// cnt[e] = local slots, off[0..E] = padded offsets. Work items are distributed over
+// `worker` in [0, nworkers) threads.
+__device__ void fill_tail(const int* cnt, const int* off, int E, int block_m, int64_t n, int64_t cap,
+                          int64_t nblocks, int32_t* sorted_ids, int32_t* expert_ids,
+                          int64_t worker, int64_t nworkers) {
+  const int ntp = off[E];
+  // padding slots inside each expert's region
+  for (int e = int(worker); e < E; e += int(nworkers)) {
+    for (int i = off[e] + cnt[e]; i < off[e + 1]; ++i) sorted_ids[i] = int32_t(n);
+  }
+  for (int64_t i = ntp + worker; i < cap; i += nworkers) sorted_ids[i] = int32_t(n);
+  const int64_t used_blocks = ntp / block_m;
+  for (int64_t b = worker; b < nblocks; b += nworkers) {
+    int val = -1;
+    if (b < used_blocks) {
+      // largest e with off[e] <= b*block_m (experts with empty regions are skipped)
+      const int row = int(b * block_m);
+      int lo = 0, hi = E - 1;
+      while (lo < hi) {
+        int mid = (lo + hi + 1) >> 1;
+        if (off[mid] <= row) lo = mid; else hi = mid - 1;
+      }
+      val = lo;
+    }
+    expert_ids[b] = val;
+  }
+}
+
+template <int C, int MAXS>
+__global__ void __launch_bounds__(1024) align_cluster_kernel(
+    const int32_t* ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
+    int32_t* expert_ids, int32_t* ntp_out, int32_t* offsets_out) {
   extern __shared__ int smem[];
-  align_single_body(ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp_out, offsets_out, smem);
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int rank = C > 1 ? int(cluster_rank()) : 0;
+  align_body<C, 32, MAXS>(ids, n, n * rank / C, n * (rank + 1) / C, rank, E, block_m, cap, nblocks, sorted_ids,
+                          expert_ids, ntp_out, offsets_out, smem);
+}
+
+template <int C, int MAXS>
+cudaError_t launch_cluster(const int32_t* ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks,
+                           int32_t* sorted_ids, int32_t* expert_ids, int32_t* ntp, int32_t* offsets,
+                           cudaStream_t stream) {
+  auto kern = align_cluster_kernel<C, MAXS>;
+  const size_t smem = align_smem_bytes<32>(E);
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, kern, ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets);
+  count_launches(1);
+  return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 // ---- router: top-k softmax routing, one warp per token ------------------------------
@@ -165,8 +278,8 @@ __global__ void __launch_bounds__(1024) router_align_single_kernel(
   extern __shared__ int smem[];
   route_tokens_any(logits, T, G, k, topk_ids, topk_weights, threadIdx.x >> 5, blockDim.x >> 5, threadIdx.x & 31);
   __syncthreads();
-  align_single_body(topk_ids, T * k, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp_out, offsets_out,
-                    smem);
+  align_body<1, 32, 1>(topk_ids, T * k, 0, T * k, 0, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp_out,
+                       offsets_out, smem);
 }
 
 
@@ -232,30 +345,6 @@ __global__ void __launch_bounds__(1024) align_scan_kernel(int E, int64_t G, int*
   if (lane == 0) cnt_g[e] = run;
 }
 
-// Exclusive prefix of vals[0, count) in place for any count (each thread sums a run of
-// consecutive values, the runs' sums are scanned across the block); returns the total.
-// tmp holds blockDim.x ints, warp_sums 33.
-__device__ int block_exclusive_scan_runs(int* vals, int count, int* tmp, int* warp_sums) {
-  const int tid = threadIdx.x;
-  const int per = (count + int(blockDim.x) - 1) / int(blockDim.x);
-  const int b = tid * per;
-  int sum = 0;
-  for (int i = 0; i < per; ++i)
-    if (b + i < count) sum += vals[b + i];
-  tmp[tid] = sum;
-  __syncthreads();
-  const int total = block_exclusive_scan(tmp, int(blockDim.x), warp_sums);
-  int run = tmp[tid];
-  for (int i = 0; i < per; ++i)
-    if (b + i < count) {
-      const int x = vals[b + i];
-      vals[b + i] = run;
-      run += x;
-    }
-  __syncthreads();
-  return total;
-}
-
 __global__ void __launch_bounds__(32 * kWarpsPerCta) align_scatter_kernel(
     const int32_t* __restrict__ ids, int64_t n, int E, int block_m, int64_t G, int64_t cap,
     int64_t nblocks, int csz, const int* __restrict__ chunk_hist, const int* __restrict__ cnt_g,
@@ -305,16 +394,13 @@ size_t align_workspace_bytes(int64_t n, int E) {
 cudaError_t launch_align(const int32_t* ids, int64_t n, int E, int block_m, int64_t cap,
                          int64_t nblocks, int32_t* sorted_ids, int32_t* expert_ids, int32_t* ntp,
                          int32_t* offsets, void* workspace, cudaStream_t stream) {
-  if ((n + kChunk - 1) / kChunk <= kSingleMaxChunks) {
-    const size_t smem = align_single_smem_bytes(E);
-    cudaError_t err = cudaFuncSetAttribute(align_single_kernel,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (err != cudaSuccess) return err;
-    align_single_kernel<<<1, 1024, smem, stream>>>(ids, n, E, block_m, cap, nblocks, sorted_ids,
-                                                   expert_ids, ntp, offsets);
-    count_launches(1);
-    return cudaGetLastError();
-  }
+  if ((n + kChunk - 1) / kChunk <= kSingleMaxChunks)
+    return launch_cluster<1, kSingleMaxChunks>(ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets,
+                                               stream);
+  if (n <= int64_t(kSortCtas) * 32 * 32 * 8)
+    return launch_cluster<kSortCtas, 8>(ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
+  if (n <= kClusterMaxSlots)
+    return launch_cluster<kSortCtas, 32>(ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
   const int csz = multi_chunk(n, E);
   const int64_t G = (n + csz - 1) / csz;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -345,7 +431,7 @@ cudaError_t launch_router_align(const float* logits, int64_t T, int G, int k, in
   const int64_t n = T * k;
   const int64_t G_chunks = (n + kChunk - 1) / kChunk;
   if (T <= kFusedMaxTokens && G_chunks <= kSingleMaxChunks) {
-    const size_t smem = align_single_smem_bytes(E);
+    const size_t smem = align_smem_bytes<32>(E);
     cudaError_t err = cudaFuncSetAttribute(router_align_single_kernel,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (err != cudaSuccess) return err;

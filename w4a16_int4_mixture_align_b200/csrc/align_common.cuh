@@ -1,14 +1,20 @@
-// align_common.cuh -- the block-padded routing sort by one CTA, shared by the sort kernels
-// and the routers that sort in the same launch. The method is described in align.cu.
+// align_common.cuh -- the block-padded routing sort by one CTA or one cluster, shared by the
+// sort kernels and the routers that sort in the same launch. The method is described in
+// align.cu.
 #pragma once
 
 #include "chord_internal.cuh"
+#include "tc_common.cuh"
 
 namespace chord {
 namespace {
 
-constexpr int kChunk = 1024;       // flat slots per warp chunk (largest)
-constexpr int kSteps = kChunk / 32;
+
+__device__ __forceinline__ int ld_cluster_i32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ bool is_local(int e, int E) { return unsigned(e) < unsigned(E); }
 
@@ -29,54 +35,6 @@ __host__ __device__ inline int key_bits(int E) {
   while ((1 << b) <= E) ++b;  // keys 0..E fit in b bits
   return b;
 }
-
-// Loads the ids of `steps` (<= kSteps) 32-slot steps starting at c0, all up front so the
-// loads overlap; slots past n read as -1 (not local).
-__device__ __forceinline__ void load_steps(const int32_t* ids, int64_t n, int64_t c0, int steps,
-                                           int v[kSteps]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t f = c0 + int64_t(s) * 32 + lane;
-    v[s] = (s < steps && f < n) ? __ldg(ids + f) : -1;
-  }
-}
-
-// hist_row[e] += number of local slots of expert e among the loaded steps (warp-cooperative).
-// Non-local slots carry key E.
-__device__ __forceinline__ void chunk_count(const int v[kSteps], int steps, int E, int nbits,
-                                            int* hist_row) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    if (s >= steps) break;
-    const int e = v[s];
-    const bool loc = is_local(e, E);
-    const unsigned peers = peers_of(loc ? unsigned(e) : unsigned(E), nbits);
-    if (loc && lane == __ffs(peers) - 1) hist_row[e] += __popc(peers);
-    __syncwarp();
-  }
-}
-
-// Places every local slot of the loaded steps at run_row[e] + (rank inside the expert),
-// advancing run_row[e]. Ranks follow increasing flat index.
-__device__ __forceinline__ void chunk_scatter(const int v[kSteps], int steps, int64_t c0, int E,
-                                              int nbits, int* run_row, int32_t* sorted_ids) {
-  const int lane = threadIdx.x & 31;
-  const unsigned lower = (1u << lane) - 1u;
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    if (s >= steps) break;
-    const int e = v[s];
-    const bool loc = is_local(e, E);
-    const unsigned peers = peers_of(loc ? unsigned(e) : unsigned(E), nbits);
-    if (loc) sorted_ids[run_row[e] + __popc(peers & lower)] = int32_t(c0 + int64_t(s) * 32 + lane);
-    __syncwarp();
-    if (loc && lane == __ffs(peers) - 1) run_row[e] += __popc(peers);
-    __syncwarp();
-  }
-}
-
 
 // Exclusive prefix sum over vals[0..count) in shared memory (count <= blockDim.x <= 1024),
 // returns the total. All threads of the block must call it.
@@ -110,87 +68,147 @@ __device__ int block_exclusive_scan(int* vals, int count, int* warp_sums) {
   return total;
 }
 
-// Sentinel fill and expert_ids, shared by both paths.
-// cnt[e] = local slots, off[0..E] = padded offsets. Work items are distributed over
-// `worker` in [0, nworkers) threads.
-__device__ void fill_tail(const int* cnt, const int* off, int E, int block_m, int64_t n, int64_t cap,
-                          int64_t nblocks, int32_t* sorted_ids, int32_t* expert_ids,
-                          int64_t worker, int64_t nworkers) {
-  const int ntp = off[E];
-  // padding slots inside each expert's region
-  for (int e = int(worker); e < E; e += int(nworkers)) {
-    for (int i = off[e] + cnt[e]; i < off[e + 1]; ++i) sorted_ids[i] = int32_t(n);
+// Exclusive prefix of vals[0, count) in place for any count (each thread sums a run of
+// consecutive values, the runs' sums are scanned across the block); returns the total.
+// tmp holds blockDim.x ints, warp_sums 33.
+__device__ int block_exclusive_scan_runs(int* vals, int count, int* tmp, int* warp_sums) {
+  const int tid = threadIdx.x;
+  const int per = (count + int(blockDim.x) - 1) / int(blockDim.x);
+  const int b = tid * per;
+  int sum = 0;
+  for (int i = 0; i < per; ++i)
+    if (b + i < count) sum += vals[b + i];
+  tmp[tid] = sum;
+  __syncthreads();
+  const int total = block_exclusive_scan(tmp, int(blockDim.x), warp_sums);
+  int run = tmp[tid];
+  for (int i = 0; i < per; ++i)
+    if (b + i < count) {
+      const int x = vals[b + i];
+      vals[b + i] = run;
+      run += x;
+    }
+  __syncthreads();
+  return total;
+}
+
+// ---- the whole sort by one CTA or one cluster ----------------------------------------
+//
+// C CTAs (rank: this one's number) of NW warps each. A CTA sorts the flat slots [begin, end);
+// the CTAs' ranges follow one another and cover [0, n). Warp w of a CTA owns `steps`
+// consecutive 32-slot steps (steps <= MAXS) and counts them by expert in its row of `hist`;
+// a prefix over the warps (one warp per expert, a lane per row), over the CTAs' totals
+// (distributed shared memory) and over the experts' padded totals then gives every warp the
+// position of its first slot of each expert. `smem`: align_smem_bytes().
+template <int NW>
+__host__ __device__ inline size_t align_smem_bytes(int E) {
+  return (size_t(NW) * E + 3 * E + E + 1 + 32 * NW + 33) * sizeof(int);
+}
+
+template <int C, int NW, int MAXS>
+__device__ __forceinline__ void align_body(const int32_t* ids, int64_t n, int64_t begin, int64_t end, int rank, int E,
+                                           int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
+                                           int32_t* expert_ids, int32_t* ntp_out, int32_t* offsets_out, int* smem) {
+  static_assert(NW <= 32, "a lane per warp's row");
+  int* hist = smem;              // [NW][E]
+  int* own = hist + NW * E;      // [E] this CTA's slots of each expert
+  int* cnt = own + E;            // [E] all of them
+  int* base = cnt + E;           // [E] position of this CTA's first slot
+  int* off = base + E;           // [E + 1] position of the expert's first slot
+  int* tmp = off + E + 1;        // [32 * NW]
+  int* wsum = tmp + 32 * NW;     // [33]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned lower = (1u << lane) - 1u;
+  for (int i = tid; i < NW * E; i += 32 * NW) hist[i] = 0;
+  __syncthreads();
+
+  const int nbits = key_bits(E);
+  const int steps = int((end - begin + 32 * NW - 1) / (32 * NW));
+  const int64_t c0 = begin + int64_t(warp) * steps * 32;
+  int* row = hist + warp * E;
+  int v[MAXS];
+#pragma unroll
+  for (int s = 0; s < MAXS; ++s) {  // all loads at once
+    const int64_t f = c0 + 32 * s + lane;
+    v[s] = s < steps && f < end ? ids[f] : -1;
   }
-  for (int64_t i = ntp + worker; i < cap; i += nworkers) sorted_ids[i] = int32_t(n);
-  const int64_t used_blocks = ntp / block_m;
-  for (int64_t b = worker; b < nblocks; b += nworkers) {
+#pragma unroll
+  for (int s = 0; s < MAXS; ++s) {
+    if (s >= steps) break;
+    const bool loc = is_local(v[s], E);
+    const unsigned peers = peers_of(loc ? unsigned(v[s]) : unsigned(E), nbits);
+    if (loc && lane == __ffs(peers) - 1) row[v[s]] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+
+  for (int e = warp; e < E; e += NW) {
+    const int c = lane < NW ? hist[lane * E + e] : 0;
+    int incl = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane < NW) hist[lane * E + e] = incl - c;
+    if (lane == 31) own[e] = incl;
+  }
+  if (C > 1) cluster_sync_all();
+  else __syncthreads();
+  for (int e = tid; e < E; e += 32 * NW) {
+    int before = 0, total = 0;
+    for (int r = 0; r < C; ++r) {
+      const int c = C > 1 ? ld_cluster_i32(cluster_addr(own + e, r)) : own[e];
+      total += c;
+      before += r < rank ? c : 0;
+    }
+    cnt[e] = total;
+    off[e] = (total + block_m - 1) / block_m * block_m;
+    base[e] = before;
+  }
+  __syncthreads();
+  const int total = block_exclusive_scan_runs(off, E, tmp, wsum);
+  if (tid == 0) off[E] = total;
+  for (int e = tid; e < E; e += 32 * NW) base[e] += off[e];
+  __syncthreads();
+
+#pragma unroll
+  for (int s = 0; s < MAXS; ++s) {
+    if (s >= steps) break;
+    const int e = v[s];
+    const bool loc = is_local(e, E);
+    const unsigned peers = peers_of(loc ? unsigned(e) : unsigned(E), nbits);
+    if (loc) sorted_ids[base[e] + row[e] + __popc(peers & lower)] = int32_t(c0 + 32 * s + lane);
+    __syncwarp();
+    if (loc && lane == __ffs(peers) - 1) row[e] += __popc(peers);
+    __syncwarp();
+  }
+  // sentinels: a warp per expert's padding, then the tail; expert_ids: a thread per block
+  const int threads = C * 32 * NW, worker = rank * 32 * NW + tid;
+  for (int e = rank * NW + warp; e < E; e += C * NW)
+    for (int i = off[e] + cnt[e] + lane; i < off[e + 1]; i += 32) sorted_ids[i] = int32_t(n);
+  for (int64_t i = total + worker; i < cap; i += threads) sorted_ids[i] = int32_t(n);
+  for (int64_t b = worker; b < nblocks; b += threads) {
     int val = -1;
-    if (b < used_blocks) {
+    if (b * block_m < total) {
       // largest e with off[e] <= b*block_m (experts with empty regions are skipped)
-      const int row = int(b * block_m);
       int lo = 0, hi = E - 1;
       while (lo < hi) {
-        int mid = (lo + hi + 1) >> 1;
-        if (off[mid] <= row) lo = mid; else hi = mid - 1;
+        const int mid = (lo + hi + 1) >> 1;
+        if (off[mid] <= int(b * block_m)) lo = mid;
+        else hi = mid - 1;
       }
       val = lo;
     }
     expert_ids[b] = val;
   }
-}
-
-// ---- single CTA (n <= kSingleMaxChunks chunks) ---------------------------------------
-// The whole sort by one CTA of 1024 threads; `smem` holds (32 + 2) * E + 34 ints.
-__device__ __forceinline__ void align_single_body(
-    const int32_t* __restrict__ ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks,
-    int32_t* __restrict__ sorted_ids, int32_t* __restrict__ expert_ids, int32_t* __restrict__ ntp_out,
-    int32_t* __restrict__ offsets_out, int* smem) {
-  int* hist = smem;                 // [32][E]
-  int* cnt = hist + 32 * E;         // [E]
-  int* off = cnt + E;               // [E+1]
-  int* wsum = off + E + 1;          // [33]
-  const int tid = threadIdx.x, warp = tid >> 5;
-  for (int i = tid; i < 32 * E; i += blockDim.x) hist[i] = 0;
-  __syncthreads();
-
-  // warp w owns `steps` consecutive 32-slot steps, so every warp works even for small n
-  const int nbits = key_bits(E);
-  const int steps = int((n + 32 * 32 - 1) / (32 * 32));
-  const int64_t c0 = int64_t(warp) * steps * 32;
-  int v[kSteps];
-  load_steps(ids, n, c0, steps, v);
-  if (c0 < n) chunk_count(v, steps, E, nbits, hist + warp * E);
-  __syncthreads();
-
-  for (int e = tid; e < E; e += blockDim.x) {
-    int run = 0;
-    for (int w = 0; w < 32; ++w) {
-      int c = hist[w * E + e];
-      hist[w * E + e] = run;
-      run += c;
-    }
-    cnt[e] = run;
-    off[e] = (run + block_m - 1) / block_m * block_m;
-  }
-  __syncthreads();
-  const int total = block_exclusive_scan(off, E, wsum);
-  if (tid == 0) off[E] = total;
-  for (int i = tid; i < 32 * E; i += blockDim.x) hist[i] += off[i % E];
-  __syncthreads();
-
-  if (c0 < n) chunk_scatter(v, steps, c0, E, nbits, hist + warp * E, sorted_ids);
-  fill_tail(cnt, off, E, block_m, n, cap, nblocks, sorted_ids, expert_ids, tid, blockDim.x);
-  if (tid == 0) {
-    ntp_out[0] = off[E];
+  if (worker == 0) {
+    ntp_out[0] = total;
     ntp_out[1] = routing_tag(block_m);
   }
   if (offsets_out)
-    for (int e = tid; e <= E; e += blockDim.x) offsets_out[e] = off[e];
-}
-
-// Dynamic shared memory of align_single_body.
-__host__ __device__ inline size_t align_single_smem_bytes(int E) {
-  return (size_t(32) * E + E + E + 1 + 33) * sizeof(int);
+    for (int e = worker; e <= E; e += threads) offsets_out[e] = off[e];
+  if (C > 1) cluster_sync_all();  // `own` has been read before its CTA ends
 }
 
 }  // namespace

@@ -52,24 +52,24 @@ __device__ __forceinline__ V warp_sum(V v) {
   return v;
 }
 
-// The logit as FP32, -inf where it masks its expert, +inf as the largest finite value.
+constexpr float kLowestF32 = -3.402823466e38f, kLowestBf16 = -3.38953139e38f, kLowestF16 = -65504.f;
+// The logit, -inf where it masks its expert, +inf as the largest finite value.
+__device__ __forceinline__ float masked_logit(float v, float lowest) { return v > lowest ? fminf(v, -lowest) : -INFINITY; }
 __device__ __forceinline__ float load_logit(const RouterArgs& p, int64_t row, int e) {
-  if (p.dtype == CHORD_DTYPE_F32) {
-    const float v = __ldg(static_cast<const float*>(p.logits) + row + e);
-    return v > -3.402823466e38f ? fminf(v, 3.402823466e38f) : -INFINITY;
-  }
-  if (p.dtype == CHORD_DTYPE_BF16) {
-    const float v = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p.logits) + row + e)) << 16);
-    return v > -3.38953139e38f ? fminf(v, 3.38953139e38f) : -INFINITY;
-  }
-  const float v = __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t*>(p.logits) + row + e)));
-  return v > -65504.f ? fminf(v, 65504.f) : -INFINITY;
+  if (p.dtype == CHORD_DTYPE_F32) return masked_logit(__ldg(static_cast<const float*>(p.logits) + row + e), kLowestF32);
+  const uint16_t bits = __ldg(static_cast<const uint16_t*>(p.logits) + row + e);
+  if (p.dtype == CHORD_DTYPE_BF16) return masked_logit(__uint_as_float(uint32_t(bits) << 16), kLowestBf16);
+  return masked_logit(__half2float(__ushort_as_half(bits)), kLowestF16);
 }
 
 // s in FP64. `lmax` and `z` (the softmax denominator) are unused for sigmoid.
-__device__ __forceinline__ double score64(const RouterArgs& p, float l, float lmax, double z) {
-  if (p.score == CHORD_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-double(l)));
+// Not inlined: its code is long, it is used in several places, and a router call runs it cold.
+__device__ __noinline__ double score64_of(int score, float l, float lmax, double z) {
+  if (score == CHORD_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-double(l)));
   return exp(double(l) - double(lmax)) / z;
+}
+__device__ __forceinline__ double score64(const RouterArgs& p, float l, float lmax, double z) {
+  return score64_of(p.score, l, lmax, z);
 }
 
 // The softmax denominator of token t in FP64 (1 if every logit is masked).
@@ -105,6 +105,7 @@ __device__ __forceinline__ uint32_t kept_groups(const RouterArgs& p, const V* v,
         a2 = x;
       }
     }
+#pragma unroll 1
   for (int o = 1; o < width; o <<= 1) {
     const V b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
     const V lo = a1 < b1 ? a1 : b1;
@@ -126,6 +127,7 @@ __device__ __forceinline__ uint32_t kept_groups(const RouterArgs& p, const V* v,
   const double mine = __shfl_sync(kFull, score, (lane * width) & 31);
   const double mine_off = __shfl_sync(kFull, off, (lane * width) & 31);
   int rank = 0;
+#pragma unroll 1
   for (int i = 0; i < p.n_group; ++i) {
     const double o = __shfl_sync(kFull, mine, i);
     rank += (o > mine || (o == mine && i < lane)) ? 1 : 0;
@@ -263,10 +265,20 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
   float* cand_l = reinterpret_cast<float*>(cand_e + 32);
 
   float l[PER], c[PER];
+  if (p.dtype == CHORD_DTYPE_F32) {
+    const float* row = static_cast<const float*>(p.logits) + t * p.ld;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < p.G ? load_logit(p, t * p.ld, e) : -INFINITY;
+    for (int i = 0; i < PER; ++i) l[i] = lane + 32 * i < p.G ? masked_logit(__ldg(row + lane + 32 * i), kLowestF32) : -INFINITY;
+  } else {
+    const uint16_t* row = static_cast<const uint16_t*>(p.logits) + t * p.ld;
+    const bool half = p.dtype == CHORD_DTYPE_F16;
+    const float lowest = half ? kLowestF16 : kLowestBf16;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t bits = lane + 32 * i < p.G ? __ldg(row + lane + 32 * i) : 0u;
+      const float v = half ? __half2float(__ushort_as_half(uint16_t(bits))) : __uint_as_float(bits << 16);
+      l[i] = lane + 32 * i < p.G ? masked_logit(v, lowest) : -INFINITY;
+    }
   }
   float lmax = 0.f;
   double z = 1.0;
@@ -279,7 +291,7 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
     if (p.bias || !p.renormalize) {
       float zf = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) zf += expf(l[i] - lmax);  // exp(-inf) = 0 for masked experts
+      for (int i = 0; i < PER; ++i) zf += __expf(l[i] - lmax);  // exp(-inf) = 0 for masked experts
       zf = warp_sum(zf);
       z = zf > 0.f ? double(zf) : 1.0;
     }
@@ -292,7 +304,7 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
       float v = -INFINITY;
       if (l[i] > -INFINITY) {
         const float s = p.score == CHORD_SCORE_SIGMOID ? __fdividef(1.f, 1.f + __expf(-fminf(fmaxf(l[i], -80.f), 80.f)))
-                                                       : expf(l[i] - lmax) * rz;
+                                                       : __expf(l[i] - lmax) * rz;
         v = s + __ldg(p.bias + e);
       }
       c[i] = v;
@@ -386,53 +398,86 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
 __host__ __device__ inline size_t router_scratch_bytes(int G) { return size_t(G) * 8 + 32 * 8; }
 
 template <int PER>
-__global__ void __launch_bounds__(32 * kRouterWarps) router_scored_kernel(const __grid_constant__ RouterArgs p) {
+__global__ void __launch_bounds__(32 * kRouterWarps, PER <= 16 ? 4 : 2) router_scored_kernel(const __grid_constant__ RouterArgs p) {
   extern __shared__ __align__(16) uint8_t router_smem[];
+  grid_dep_wait();
+  grid_dep_trigger();
   const int warp = threadIdx.x >> 5;
   uint8_t* scratch = router_smem + warp * router_scratch_bytes(p.G);
   for (int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp; t < p.T; t += int64_t(gridDim.x) * kRouterWarps)
     route_token<PER>(p, t, scratch);
 }
 
-// Up to kRouterWarps tokens: one CTA routes them, one warp each, then sorts the ids.
-template <int PER>
-__global__ void __launch_bounds__(1024) router_scored_align_kernel(const __grid_constant__ RouterArgs p, int E,
-                                                                   int block_m, int64_t cap, int64_t nblocks,
-                                                                   int32_t* __restrict__ sorted_ids,
-                                                                   int32_t* __restrict__ expert_ids,
-                                                                   int32_t* __restrict__ ntp,
-                                                                   int32_t* __restrict__ offsets) {
+// Decode batches in one launch: C CTAs (a cluster) route T / C tokens each, a warp per token,
+// then sort the ids together.
+constexpr int kFusedWarps = 16;
+constexpr int kFusedCtas = 8;
+constexpr int kFusedMaxTokens = 2 * kFusedCtas * kFusedWarps;  // two rounds of tokens a warp
+constexpr int kFusedMaxSteps = 4;  // 32 tokens x 64 slots a CTA, over 16 x 32 lanes
+
+template <int PER, int C>
+__global__ void __launch_bounds__(32 * kFusedWarps) router_scored_align_kernel(
+    const __grid_constant__ RouterArgs p, int E, int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
+    int32_t* expert_ids, int32_t* ntp, int32_t* offsets) {
   extern __shared__ __align__(16) uint8_t router_smem[];
+  grid_dep_wait();
+  grid_dep_trigger();
   const int warp = threadIdx.x >> 5;
-  if (warp < p.T) route_token<PER>(p, warp, router_smem + warp * router_scratch_bytes(p.G));
+  const int rank = C > 1 ? int(cluster_rank()) : 0;
+  const int64_t t0 = p.T * rank / C, t1 = p.T * (rank + 1) / C;
+#pragma unroll 1
+  for (int64_t t = t0 + warp; t < t1; t += kFusedWarps)
+    route_token<PER>(p, t, router_smem + warp * router_scratch_bytes(p.G));
   __syncthreads();
-  align_single_body(p.topk_ids, p.T * p.k, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets,
-                    reinterpret_cast<int*>(router_smem));
+  align_body<C, kFusedWarps, kFusedMaxSteps>(p.topk_ids, p.T * p.k, t0 * p.k, t1 * p.k, rank, E, block_m, cap, nblocks,
+                                             sorted_ids, expert_ids, ntp, offsets,
+                                             reinterpret_cast<int*>(router_smem));
+}
+
+template <int PER, int C>
+cudaError_t launch_fused(const RouterArgs& p, int E, int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
+                         int32_t* expert_ids, int32_t* ntp, int32_t* offsets, cudaStream_t stream) {
+  auto kern = router_scored_align_kernel<PER, C>;
+  const size_t route = router_scratch_bytes(p.G) * kFusedWarps, sort = align_smem_bytes<kFusedWarps>(E);
+  const size_t smem = route > sort ? route : sort;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(32 * kFusedWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, kern, p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets);
+  count_launches(1);
+  return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 template <int PER>
 cudaError_t launch_per(const RouterArgs& p, int E, int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
                        int32_t* expert_ids, int32_t* ntp, int32_t* offsets, void* workspace, int num_sms,
                        cudaStream_t stream) {
+  if (p.T <= kFusedWarps)
+    return launch_fused<PER, 1>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
+  if (p.T <= kFusedMaxTokens)
+    return launch_fused<PER, kFusedCtas>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
   const size_t route = router_scratch_bytes(p.G) * kRouterWarps;
-  if (p.T <= kRouterWarps) {
-    size_t smem = align_single_smem_bytes(E);
-    if (route > smem) smem = route;
-    cudaError_t err = cudaFuncSetAttribute(router_scored_align_kernel<PER>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (err != cudaSuccess) return err;
-    router_scored_align_kernel<PER><<<1, 1024, smem, stream>>>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids,
-                                                               ntp, offsets);
-    count_launches(1);
-    return cudaGetLastError();
-  }
   cudaError_t err = cudaFuncSetAttribute(router_scored_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(route));
   if (err != cudaSuccess) return err;
   const int64_t want = (p.T + kRouterWarps - 1) / kRouterWarps, most = int64_t(num_sms) * 8;
-  router_scored_kernel<PER><<<unsigned(want < most ? want : most), 32 * kRouterWarps, route, stream>>>(p);
+  err = launch_pdl(true, router_scored_kernel<PER>, dim3(unsigned(want < most ? want : most)), dim3(32 * kRouterWarps),
+                   route, stream, p);
   count_launches(1);
-  err = cudaGetLastError();
+  if (err == cudaSuccess) err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   return launch_align(p.topk_ids, p.T * p.k, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets,
                       workspace, stream);
