@@ -72,7 +72,17 @@ __device__ __forceinline__ void block_scale(uint32_t amax_bits, float* scale, fl
   *scale = finite ? __fdiv_rn(amax, kFp8Max) : nan;
   *inverse = finite ? __fdiv_rn(kFp8Max, amax) : nan;
 }
-__device__ __forceinline__ float silu_times(float g, float u) { return __fdiv_rn(g, 1.f + expf(-g)) * u; }
+// silu(g) * u. The reciprocal of d = 1 + exp(-g) is the hardware's approximation and one step
+// of Newton's iteration, half the instructions of a division; below -80, where exp(-g) nears
+// the end of the range, 1/d is exp(g) to FP32.
+__device__ __forceinline__ float silu_times(float g, float u) {
+  if (g < -80.f) return g * expf(g) * u;
+  const float d = 1.f + expf(-g);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  r = fmaf(r, fmaf(-d, r, 1.f), r);
+  return g * r * u;
+}
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t stream);

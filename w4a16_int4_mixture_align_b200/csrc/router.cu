@@ -45,6 +45,7 @@ __device__ __forceinline__ float order_value(uint32_t k) {
   return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 __device__ __forceinline__ float warp_max(float v) { return order_value(__reduce_max_sync(kFull, order_key(v))); }
+__device__ __forceinline__ float warp_min(float v) { return order_value(__reduce_min_sync(kFull, order_key(v))); }
 template <typename V>
 __device__ __forceinline__ V warp_sum(V v) {
 #pragma unroll
@@ -62,17 +63,29 @@ __device__ __forceinline__ float load_logit(const RouterArgs& p, int64_t row, in
   return masked_logit(__half2float(__ushort_as_half(bits)), kLowestF16);
 }
 
-// s in FP64. `lmax` and `z` (the softmax denominator) are unused for sigmoid.
-// Not inlined: its code is long, it is used in several places, and a router call runs it cold.
-__device__ __noinline__ double score64_of(int score, float l, float lmax, double z) {
-  if (score == CHORD_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-double(l)));
-  return exp(double(l) - double(lmax)) / z;
+// 1 / d for 2^-100 <= d <= 2^100, within a few 2^-52: Newton's iteration r <- r (2 - d r) doubles the 23 bits of an
+// FP32 reciprocal twice.
+__device__ __forceinline__ double reciprocal64(double d) {
+  double r = double(1.0f / float(d));
+  r = fma(r, fma(-d, r, 1.0), r);
+  return fma(r, fma(-d, r, 1.0), r);
 }
-__device__ __forceinline__ double score64(const RouterArgs& p, float l, float lmax, double z) {
-  return score64_of(p.score, l, lmax, z);
+// s in FP64; `lmax` and `rz` (one over the softmax denominator) are unused for sigmoid. Not
+// inlined: the code is long, it is used in several places, and a small call runs it cold.
+__device__ __noinline__ double score64_of(int score, float l, float lmax, double rz) {
+  if (score == CHORD_SCORE_SOFTMAX) return exp(double(l) - double(lmax)) * rz;
+  return 1.0 / (1.0 + exp(-double(l)));
+}
+__device__ __forceinline__ double score64(const RouterArgs& p, float l, float lmax, double rz) {
+  return score64_of(p.score, l, lmax, rz);
+}
+// s in FP32, within 1e-6.
+__device__ __forceinline__ float score32(const RouterArgs& p, float l, float lmax, float rz) {
+  if (p.score == CHORD_SCORE_SOFTMAX) return __expf(l - lmax) * rz;
+  return __fdividef(1.f, 1.f + __expf(-fminf(fmaxf(l, -80.f), 80.f)));
 }
 
-// The softmax denominator of token t in FP64 (1 if every logit is masked).
+// One over the softmax denominator of token t in FP64 (1 if every logit is masked).
 __device__ __noinline__ double softmax_sum64(const RouterArgs& p, int64_t t, float lmax) {
   double z = 0.0;
   for (int e = threadIdx.x & 31; e < p.G; e += 32) {
@@ -80,31 +93,31 @@ __device__ __noinline__ double softmax_sum64(const RouterArgs& p, int64_t t, flo
     if (l > -INFINITY) z += exp(double(l) - double(lmax));
   }
   z = warp_sum(z);
-  return z > 0.0 ? z : 1.0;
+  return z > 0.0 ? 1.0 / z : 1.0;
 }
 
 // The kept groups of the token as a bit mask, from the keys v[0..G) in shared memory
-// (-inf: masked). `near` reports a border that the keys' error could move. A team of
-// 32 / (n_group rounded up to a power of two) lanes scans each group.
+// (-inf: masked); V = float: approximate scores, `near` reports a border that their error
+// could move; V = double: exact. A team of 32 / (n_group rounded up to a power of two) lanes
+// scans each group.
 template <typename V>
-__device__ __forceinline__ uint32_t kept_groups(const RouterArgs& p, const V* v, float lmax, double slack_abs,
-                                                double slack_rel, bool* near) {
+__device__ __forceinline__ uint32_t kept_groups(const RouterArgs& p, const V* v, float lmax, bool* near) {
   const int lane = threadIdx.x & 31;
   int teams = 1;
   while (teams < p.n_group) teams <<= 1;
   const int width = 32 / teams;
   const int g = lane / width, sub = lane % width;
   V a1 = V(-INFINITY), a2 = V(-INFINITY);
-  if (g < p.n_group)
+  if (g < p.n_group) {
+    const V* of = v + g * p.group_size;
+#pragma unroll 4
     for (int j = sub; j < p.group_size; j += width) {
-      const V x = v[g * p.group_size + j];
-      if (x > a1) {
-        a2 = a1;
-        a1 = x;
-      } else if (x > a2) {
-        a2 = x;
-      }
+      const V x = of[j];
+      const V lo = x < a1 ? x : a1;
+      a1 = x < a1 ? a1 : x;
+      a2 = a2 < lo ? lo : a2;
     }
+  }
 #pragma unroll 1
   for (int o = 1; o < width; o <<= 1) {
     const V b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
@@ -113,97 +126,96 @@ __device__ __forceinline__ uint32_t kept_groups(const RouterArgs& p, const V* v,
     a2 = a2 < b2 ? b2 : a2;
     a2 = a2 < lo ? lo : a2;
   }
-  double score = double(a1);
-  if (p.group_top == 2 && a1 > V(-INFINITY)) {
+  const bool any = a1 > V(-INFINITY), two = p.group_top == 2 && a2 > V(-INFINITY);
+  V score = a1;
+  float off = 0.f;  // how far `score` may be off
+  if (any && (p.group_top == 2 || p.bias)) {
     // without a bias the keys are logits: their scores add up, not they themselves (the
     // softmax denominator is common to all groups and left out)
-    const bool two = a2 > V(-INFINITY);
-    if (p.bias) score += two ? double(a2) : 0.0;
-    else score = score64(p, float(a1), lmax, 1.0) + (two ? score64(p, float(a2), lmax, 1.0) : 0.0);
+    if (!p.bias && p.group_top == 2) {
+      if constexpr (sizeof(V) == 8)
+        score = score64(p, float(a1), lmax, 1.0) + (two ? score64(p, float(a2), lmax, 1.0) : 0.0);
+      else
+        score = score32(p, a1, lmax, 1.f) + (two ? score32(p, a2, lmax, 1.f) : 0.f);
+    } else if (two) {
+      score += a2;
+    }
+    off = kSlackAbs + kSlackRel * (fabsf(float(a1)) + (two ? fabsf(float(a2)) : 0.f));
   }
-  const double size = fabs(double(a1)) + (p.group_top == 2 && a2 > V(-INFINITY) ? fabs(double(a2)) : 0.0);
-  const double off = slack_abs + slack_rel * (a1 > V(-INFINITY) ? size : 0.0);
   // lane i < n_group takes group i's score; rank by counting
-  const double mine = __shfl_sync(kFull, score, (lane * width) & 31);
-  const double mine_off = __shfl_sync(kFull, off, (lane * width) & 31);
+  V mine = __shfl_sync(kFull, score, (lane * width) & 31);
+  const float mine_off = __shfl_sync(kFull, off, (lane * width) & 31);
+  if (lane >= p.n_group) mine = V(-INFINITY);
   int rank = 0;
-#pragma unroll 1
+#pragma unroll 4
   for (int i = 0; i < p.n_group; ++i) {
-    const double o = __shfl_sync(kFull, mine, i);
+    const V o = __shfl_sync(kFull, mine, i);
     rank += (o > mine || (o == mine && i < lane)) ? 1 : 0;
   }
-  const bool real = lane < p.n_group && mine > -INFINITY;
+  const bool real = mine > V(-INFINITY);
   const uint32_t kept = __ballot_sync(kFull, real && rank < p.topk_group);
-  // in doubt where the least a kept group may have is no more than a dropped one may have
-  const bool in = (kept >> lane) & 1u;
-  double low = in ? mine - mine_off : INFINITY, high = real && !in ? mine + mine_off : -INFINITY;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    low = fmin(low, __shfl_xor_sync(kFull, low, o));
-    high = fmax(high, __shfl_xor_sync(kFull, high, o));
+  *near = false;
+  if constexpr (sizeof(V) == 4) {
+    // in doubt where the least a kept group may have is no more than a dropped one may have
+    const bool in = (kept >> lane) & 1u;
+    const float low = warp_min(in ? mine - mine_off : INFINITY);
+    const float high = warp_max(real && !in ? mine + mine_off : -INFINITY);
+    *near = high >= low && (p.bias || p.group_top == 2);
   }
-  *near = high >= low;
   return kept;
 }
 
-// Ranks this lane's candidate (lane < n; c descending, ties to the lower lane). *gap: the
-// smallest distance to another candidate that is not the same number for certain.
-__device__ __forceinline__ int rank_of(double c, int n, double* gap) {
+// Doubles as unsigned integers of the same order.
+__device__ __forceinline__ uint64_t order_key64(double v) {
+  const uint64_t b = uint64_t(__double_as_longlong(v));
+  return b ^ ((b >> 63) ? ~uint64_t(0) : uint64_t(1) << 63);
+}
+// Rank of this lane's candidate (lane < n) by c descending, ties to the lower lane. `keys`: 32
+// shared 64-bit words of this warp.
+__device__ __forceinline__ int rank_of(double c, int n, uint64_t* keys) {
   const int lane = threadIdx.x & 31;
+  const uint64_t mine = order_key64(c + 0.0);  // -0 is the same number as 0
+  __syncwarp();
+  keys[lane] = mine;  // lanes from n on hold -inf, below every candidate
+  __syncwarp();
   int rank = 0;
-  double d = INFINITY;
-  for (int j = 0; j < n; ++j) {
-    const double o = __shfl_sync(kFull, c, j);
-    rank += (o > c || (o == c && j < lane)) ? 1 : 0;
-    if (j != lane && lane < n) d = fmin(d, fabs(o - c));
+#pragma unroll 4
+  for (int j = 0; j < n; j += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(keys + j);
+    rank += (o.x > mine || (o.x == mine && j < lane)) ? 1 : 0;
+    rank += (o.y > mine || (o.y == mine && j + 1 < lane)) ? 1 : 0;
   }
-  *gap = d;
   return rank;
 }
-
-// Writes rank `rank`'s id and weight (lanes with `mine`), and empty slots from rank n on.
-__device__ __forceinline__ void write_token(const RouterArgs& p, int64_t t, bool mine, int rank, int e, float l,
-                                            float lmax, double z, int n) {
+// Whether two of the n candidates are closer than `d`.
+__device__ __forceinline__ bool any_closer(double c, int n, double d) {
   const int lane = threadIdx.x & 31;
-  double s = 0.0;
-  if (mine) {
-    if (p.renormalize && p.score == CHORD_SCORE_SOFTMAX) z = 1.0;  // cancels
-    s = score64(p, l, lmax, z);
+  bool close = false;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(kFull, c, j);
+    close = close || (j != lane && lane < n && fabs(o - c) <= d);
   }
-  if (p.renormalize) {
-    const double sum = warp_sum(s);
-    s = sum > 0.0 ? s / sum : 0.0;
-  }
-  if (mine) {
-    p.topk_ids[t * p.k + rank] = e;
-    p.topk_weights[t * p.k + rank] = float(s * double(p.scale));
-  }
-  for (int r = n + lane; r < p.k; r += 32) {
-    p.topk_ids[t * p.k + r] = -1;
-    p.topk_weights[t * p.k + r] = 0.f;
-  }
+  return __any_sync(kFull, close);
 }
 
 // Every c in FP64 (shared memory), k rounds of a warp-wide maximum.
 __device__ __noinline__ void route_exact(const RouterArgs& p, int64_t t, float lmax, double* c64) {
   const int lane = threadIdx.x & 31;
   const int per = (p.G + 31) / 32;
-  double z = 0.0;
-  if (p.score == CHORD_SCORE_SOFTMAX) {
-    z = softmax_sum64(p, t, lmax);
-  }
+  const double rz = p.score == CHORD_SCORE_SOFTMAX ? softmax_sum64(p, t, lmax) : 1.0;
   __syncwarp();
   for (int e = lane; e < p.G; e += 32) {
     const float l = load_logit(p, t * p.ld, e);
     double c = -INFINITY;
-    if (l > -INFINITY) c = p.bias ? score64(p, l, lmax, z) + double(__ldg(p.bias + e)) : double(l);
+    if (l > -INFINITY) c = p.bias ? score64(p, l, lmax, rz) + double(__ldg(p.bias + e)) : double(l);
     c64[e] = c;
   }
   __syncwarp();
   uint32_t kept = kFull;
   if (p.n_group > 1) {
     bool near;
-    kept = kept_groups<double>(p, c64, lmax, 0.0, 0.0, &near);
+    kept = kept_groups<double>(p, c64, lmax, &near);
   }
   uint32_t open = 0;  // this lane's experts that may still be chosen
   for (int i = 0; i < per; ++i) {
@@ -234,7 +246,7 @@ __device__ __noinline__ void route_exact(const RouterArgs& p, int64_t t, float l
     }
     if (be == 0x7fffffff) break;
     if ((be & 31) == lane) open &= ~(1u << (be >> 5));
-    const double s = score64(p, load_logit(p, t * p.ld, be), lmax, p.renormalize ? 1.0 : z);
+    const double s = score64(p, load_logit(p, t * p.ld, be), lmax, rz);
     sum += s;
     if (lane == 0) {
       p.topk_ids[t * p.k + n] = be;
@@ -248,20 +260,21 @@ __device__ __noinline__ void route_exact(const RouterArgs& p, int64_t t, float l
       p.topk_weights[t * p.k + r] = 0.f;
     } else if (p.renormalize) {
       const int e = p.topk_ids[t * p.k + r];
-      const double s = score64(p, load_logit(p, t * p.ld, e), lmax, 1.0);
+      const double s = score64(p, load_logit(p, t * p.ld, e), lmax, rz);
       p.topk_weights[t * p.k + r] = sum > 0.0 ? float(s / sum * double(p.scale)) : 0.f;
     }
   }
   __syncwarp();
 }
 
-// One token by one warp. `scratch`: G doubles, then 32 ints and 32 floats, of this warp.
+// One token by one warp, with router_scratch_bytes() of shared memory of its own.
 template <int PER>
 __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint8_t* scratch) {
   const int lane = threadIdx.x & 31;
   double* c64 = reinterpret_cast<double*>(scratch);
   float* c32 = reinterpret_cast<float*>(scratch);
-  int* cand_e = reinterpret_cast<int*>(scratch + size_t(p.G) * 8);
+  uint64_t* keys = reinterpret_cast<uint64_t*>(scratch + (size_t(p.G) * 8 + 15) / 16 * 16);
+  int* cand_e = reinterpret_cast<int*>(keys + 32);
   float* cand_l = reinterpret_cast<float*>(cand_e + 32);
 
   float l[PER], c[PER];
@@ -280,8 +293,12 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
       l[i] = lane + 32 * i < p.G ? masked_logit(v, lowest) : -INFINITY;
     }
   }
-  float lmax = 0.f;
-  double z = 1.0;
+  float b[PER];
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) b[i] = lane + 32 * i < p.G ? __ldg(p.bias + lane + 32 * i) : 0.f;
+  }
+  float lmax = 0.f, rz32 = 1.f;
   if (p.score == CHORD_SCORE_SOFTMAX) {
     float m = -INFINITY;
 #pragma unroll
@@ -289,30 +306,16 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
     m = warp_max(m);
     lmax = m > -INFINITY ? m : 0.f;
     if (p.bias || !p.renormalize) {
-      float zf = 0.f;
+      float z = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) zf += __expf(l[i] - lmax);  // exp(-inf) = 0 for masked experts
-      zf = warp_sum(zf);
-      z = zf > 0.f ? double(zf) : 1.0;
+      for (int i = 0; i < PER; ++i) z += expf(l[i] - lmax);  // exp(-inf) = 0 for masked experts
+      z = warp_sum(z);
+      rz32 = z > 0.f ? __fdiv_rn(1.f, z) : 1.f;
     }
   }
-  if (p.bias) {
-    const float rz = 1.0f / float(z);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      float v = -INFINITY;
-      if (l[i] > -INFINITY) {
-        const float s = p.score == CHORD_SCORE_SIGMOID ? __fdividef(1.f, 1.f + __expf(-fminf(fmaxf(l[i], -80.f), 80.f)))
-                                                       : __expf(l[i] - lmax) * rz;
-        v = s + __ldg(p.bias + e);
-      }
-      c[i] = v;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = l[i];
-  }
+  for (int i = 0; i < PER; ++i)
+    c[i] = !p.bias ? l[i] : l[i] > -INFINITY ? score32(p, l[i], lmax, rz32) + b[i] : -INFINITY;
 
   if (p.n_group > 1) {
     __syncwarp();
@@ -323,9 +326,8 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
     }
     __syncwarp();
     bool near;
-    const uint32_t kept = kept_groups<float>(p, c32, lmax, p.bias ? double(kSlackAbs) : 0.0,
-                                             p.bias ? double(kSlackRel) : 0.0, &near);
-    if (near && p.bias) {
+    const uint32_t kept = kept_groups<float>(p, c32, lmax, &near);
+    if (near) {
       route_exact(p, t, lmax, c64);
       return;
     }
@@ -336,27 +338,24 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
     }
   }
 
-  // threshold: the k-th largest lane maximum (all lanes that share a value count at once)
+  // threshold: the k-th largest lane maximum, the least of those with fewer than k above
   float thr = -INFINITY;
   bool fits = p.k <= 32;
   if (fits) {
     float best = c[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) best = fmaxf(best, c[i]);
-    uint32_t key = order_key(best);
-    const uint32_t none = order_key(-INFINITY);
-    int seen = 0;
-    for (int r = 0; r < p.k; ++r) {
-      const uint32_t m = __reduce_max_sync(kFull, key);
-      if (m == none) break;
-      seen += __popc(__ballot_sync(kFull, key == m));
-      if (seen >= p.k) {
-        thr = order_value(m);
-        break;
-      }
-      if (key == m) key = none;
+    cand_l[lane] = best;
+    __syncwarp();
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(cand_l + j);
+      above += (o.x > best) + (o.y > best) + (o.z > best) + (o.w > best);
     }
+    thr = warp_min(above < p.k ? best : INFINITY);
     if (p.bias && thr > -INFINITY) thr -= kSlackAbs + kSlackRel * fabsf(thr);
+    __syncwarp();
   }
   int n = 0;
   if (fits) {
@@ -383,22 +382,37 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
   const int e = mine ? cand_e[lane] : 0;
   const float lc = mine ? cand_l[lane] : 0.f;
   __syncwarp();
-  double key = -INFINITY, gap;
-  if (mine) key = p.bias ? score64(p, lc, lmax, z) + double(__ldg(p.bias + e)) : double(lc);
-  int rank = rank_of(key, n, &gap);
-  if (p.bias && p.score == CHORD_SCORE_SOFTMAX && __any_sync(kFull, gap <= 2.0 * kSlackAbs)) {
+  double s = 0.0, rz = double(rz32);
+  if (mine) s = score64(p, lc, lmax, rz);
+  double key = mine ? (p.bias ? s + double(__ldg(p.bias + e)) : double(lc)) : -INFINITY;
+  int rank = rank_of(key, n, keys);
+  if (p.bias && p.score == CHORD_SCORE_SOFTMAX && any_closer(key, n, 2.0 * kSlackAbs)) {
     // the denominator's FP32 error could swap two experts: once more with it in FP64
-    z = softmax_sum64(p, t, lmax);
-    if (mine) key = score64(p, lc, lmax, z) + double(__ldg(p.bias + e));
-    rank = rank_of(key, n, &gap);
+    rz = softmax_sum64(p, t, lmax);
+    if (mine) s = score64(p, lc, lmax, rz);
+    if (mine) key = s + double(__ldg(p.bias + e));
+    rank = rank_of(key, n, keys);
   }
-  write_token(p, t, mine && rank < p.k, rank, e, lc, lmax, z, n);
+  const bool chosen = mine && rank < p.k;
+  if (p.renormalize) {
+    const double sum = warp_sum(chosen ? s : 0.0);
+    s = sum > 0x1p-100 ? s * reciprocal64(sum) : sum > 0.0 ? s / sum : 0.0;
+  }
+  if (chosen) {
+    p.topk_ids[t * p.k + rank] = e;
+    p.topk_weights[t * p.k + rank] = float(s * double(p.scale));
+  }
+  for (int r = n + lane; r < p.k; r += 32) {
+    p.topk_ids[t * p.k + r] = -1;
+    p.topk_weights[t * p.k + r] = 0.f;
+  }
 }
 
-__host__ __device__ inline size_t router_scratch_bytes(int G) { return size_t(G) * 8 + 32 * 8; }
+// Of a warp: G doubles, 32 64-bit keys, 32 candidates' ids and logits.
+__host__ __device__ inline size_t router_scratch_bytes(int G) { return (size_t(G) * 8 + 15) / 16 * 16 + 32 * 16; }
 
 template <int PER>
-__global__ void __launch_bounds__(32 * kRouterWarps, PER <= 16 ? 4 : 2) router_scored_kernel(const __grid_constant__ RouterArgs p) {
+__global__ void __launch_bounds__(32 * kRouterWarps, PER <= 12 ? 4 : PER <= 16 ? 3 : 2) router_scored_kernel(const __grid_constant__ RouterArgs p) {
   extern __shared__ __align__(16) uint8_t router_smem[];
   grid_dep_wait();
   grid_dep_trigger();
