@@ -102,7 +102,7 @@ __device__ int block_exclusive_scan_runs(int* vals, int count, int* tmp, int* wa
 // position of its first slot of each expert. `smem`: align_smem_bytes().
 template <int NW>
 __host__ __device__ inline size_t align_smem_bytes(int E) {
-  return (size_t(NW) * E + 3 * E + E + 1 + 32 * NW + 33) * sizeof(int);
+  return (size_t(NW) * (E | 1) + 3 * E + E + 1 + 32 * NW + 33) * sizeof(int);
 }
 
 template <int C, int NW, int MAXS>
@@ -110,8 +110,10 @@ __device__ __forceinline__ void align_body(const int32_t* ids, int64_t n, int64_
                                            int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
                                            int32_t* expert_ids, int32_t* ntp_out, int32_t* offsets_out, int* smem) {
   static_assert(NW <= 32, "a lane per warp's row");
-  int* hist = smem;              // [NW][E]
-  int* own = hist + NW * E;      // [E] this CTA's slots of each expert
+  // rows of an odd length, so that the lanes of a column's prefix hit different banks
+  const int ldh = E | 1;
+  int* hist = smem;              // [NW][ldh]
+  int* own = hist + NW * ldh;    // [E] this CTA's slots of each expert
   int* cnt = own + E;            // [E] all of them
   int* base = cnt + E;           // [E] position of this CTA's first slot
   int* off = base + E;           // [E + 1] position of the expert's first slot
@@ -119,13 +121,13 @@ __device__ __forceinline__ void align_body(const int32_t* ids, int64_t n, int64_
   int* wsum = tmp + 32 * NW;     // [33]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned lower = (1u << lane) - 1u;
-  for (int i = tid; i < NW * E; i += 32 * NW) hist[i] = 0;
+  for (int i = tid; i < NW * ldh; i += 32 * NW) hist[i] = 0;
   __syncthreads();
 
   const int nbits = key_bits(E);
   const int steps = int((end - begin + 32 * NW - 1) / (32 * NW));
   const int64_t c0 = begin + int64_t(warp) * steps * 32;
-  int* row = hist + warp * E;
+  int* row = hist + warp * ldh;
   int v[MAXS];
 #pragma unroll
   for (int s = 0; s < MAXS; ++s) {  // all loads at once
@@ -135,32 +137,32 @@ __device__ __forceinline__ void align_body(const int32_t* ids, int64_t n, int64_
 #pragma unroll
   for (int s = 0; s < MAXS; ++s) {
     if (s >= steps) break;
-    const bool loc = is_local(v[s], E);
-    const unsigned peers = peers_of(loc ? unsigned(v[s]) : unsigned(E), nbits);
-    if (loc && lane == __ffs(peers) - 1) row[v[s]] += __popc(peers);
-    __syncwarp();
+    if (is_local(v[s], E)) atomicAdd(row + v[s], 1);  // integers: any order gives the same counts
   }
   __syncthreads();
 
+#pragma unroll 2
   for (int e = warp; e < E; e += NW) {
-    const int c = lane < NW ? hist[lane * E + e] : 0;
+    const int c = lane < NW ? hist[lane * ldh + e] : 0;
     int incl = c;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
     }
-    if (lane < NW) hist[lane * E + e] = incl - c;
+    if (lane < NW) hist[lane * ldh + e] = incl - c;
     if (lane == 31) own[e] = incl;
   }
   if (C > 1) cluster_sync_all();
   else __syncthreads();
   for (int e = tid; e < E; e += 32 * NW) {
-    int before = 0, total = 0;
+    int before = 0, total = 0, c[C];
+#pragma unroll
+    for (int r = 0; r < C; ++r) c[r] = C > 1 ? ld_cluster_i32(cluster_addr(own + e, r)) : own[e];
+#pragma unroll
     for (int r = 0; r < C; ++r) {
-      const int c = C > 1 ? ld_cluster_i32(cluster_addr(own + e, r)) : own[e];
-      total += c;
-      before += r < rank ? c : 0;
+      total += c[r];
+      before += r < rank ? c[r] : 0;
     }
     cnt[e] = total;
     off[e] = (total + block_m - 1) / block_m * block_m;
