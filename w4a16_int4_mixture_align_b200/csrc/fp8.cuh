@@ -86,8 +86,9 @@ __device__ __forceinline__ float silu_times(float g, float u) {
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t stream);
-// a.bm in {16, 32, 64, 128}; likely_units: units of bm rows the caller expects (performance only).
-cudaError_t launch_fp8_stream(const Fp8Args& a, int64_t likely_units, cudaStream_t stream);
+// a.bm in {16, 32, 64}; `split` CTAs (a power of two up to 8, at most the k blocks) share an item.
+constexpr int kFp8StreamCtas = 2;  // resident per SM
+cudaError_t launch_fp8_stream(const Fp8Args& a, int split, cudaStream_t stream);
 // a.bm in {128, 256}: single CTAs or CTA pairs.
 cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream);
 // Dense, w = [gate; up] with a.N = 2 I: SiLU(gate) * up quantised to q [rows, I], scales [I/128, rows].

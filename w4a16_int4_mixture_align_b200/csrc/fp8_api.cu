@@ -1,5 +1,7 @@
 // fp8_api.cu -- entry points of the FP8 block-128 operators: argument checks, the choice of
 // the schedule and the launch sequence.
+#include <math.h>
+
 #include "fp8.cuh"
 
 namespace chord {
@@ -70,14 +72,68 @@ Fp8Args product_args(const uint8_t* xq, const float* xs, int64_t rows, int K, co
   return a;
 }
 
-// The schedule for `expected` rows per expert, then the product.
+// CTAs that share an item of the streaming kernel: as many as keep the likely items within
+// one wave, each with two k blocks at least.
+int stream_split(int64_t items, int KB, int64_t slots) {
+  int split = 1;
+  while (split < 8 && items * split * 2 <= slots && KB >= 4 * split) split *= 2;
+  return split;
+}
+
+struct Plan {
+  bool tensor;  // the tile kernel (fp8_tile.cu) or the streaming one (fp8_stream.cu)
+  int bm;       // rows of a unit
+  int split;    // streaming: CTAs that share an item
+  double us;    // estimate
+};
+
+// The schedule with the least estimated time. An estimate is a start-up time plus, for each
+// wave of the CTAs, the k blocks of an item times a time per block (and a time per tile),
+// fitted to measurements on a B200 over M = 8 .. 4096 of 4096 x 7168, 7168 x 2048, 512 x 7168,
+// 576 x 1520 and 7168 x 256 (N x K); it lies within a quarter of them. On both sides of some
+// borders, in us: 4096 x 7168 M=128 64-row streaming 14.0, 128-row tiles 27.4, 256-row 32.2;
+// M=384 35.7, 28.9, 32.8; M=768 -, 52.3, 33.6; 512 x 7168 M=512 11.5, 27.3, 31.5.
+// `expected`: rows per expert; grouped experts are taken to hold up to 1.25 times as many, and
+// contiguous ones whole 128-row blocks.
+Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
+  const int KB = fp8_blocks(a.K);
+  const double rows = a.layout == kFp8Masked ? 1.25 * expected : double(expected);
+  auto units_of = [&](int bm) {
+    const double per = a.layout == kFp8Contiguous && bm < 128 ? ceil(rows / 128) * (128 / bm) : ceil(rows / bm);
+    return int64_t(per * (a.layout == kFp8Dense ? 1 : a.E));
+  };
+  auto waves = [](int64_t items, int64_t slots) { return double((items + slots - 1) / slots); };
+  Plan best{};
+  best.us = 1e30;
+  auto offer = [&](bool tensor, int bm, int split, double us) {
+    if (us < best.us) best = Plan{tensor, bm, split, us};
+  };
+  if (!(flags & CHORD_FLAG_FORCE_TENSOR)) {
+    const double start[3] = {4.6, 5.0, 6.4}, per_kb[3] = {0.37, 0.39, 0.52};
+    const int64_t slots = int64_t(a.num_sms) * kFp8StreamCtas, tiles = (a.N + 127) / 128;
+    for (int i = 0; i < 3; ++i) {
+      const int bm = 16 << i;
+      const int64_t items = units_of(bm) * tiles;
+      int split = stream_split(items, KB, slots);
+      // a split grid covers every unit there may be, so it has to stay small
+      const int64_t most = ((a.rows + bm - 1) / bm + (a.layout == kFp8Dense ? 0 : a.E)) * tiles;
+      if (most * split > 8 * slots) split = 1;
+      offer(false, bm, split, start[i] + waves(items * split, slots) * ((KB + split - 1) / split) * per_kb[i]);
+    }
+  }
+  if (!(flags & CHORD_FLAG_FORCE_STREAM)) {
+    offer(true, 128, 1, 2.4 + waves(units_of(128) * ((a.N + 127) / 128), a.num_sms) * (KB * 0.42 + 1.2));
+    offer(true, 256, 1, 3.0 + waves(units_of(256) * ((a.N + 255) / 256), a.num_sms / 2) * (KB * 0.54 + 0.9));
+  }
+  return best;
+}
+
+// The product by the schedule chosen for `expected` rows per expert.
 chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices, const int32_t* masked_m,
                            int64_t max_m, void* workspace, int flags, cudaStream_t stream) {
-  const bool tensor = (flags & CHORD_FLAG_FORCE_TENSOR) || (!(flags & CHORD_FLAG_FORCE_STREAM) && expected > 128);
-  if (tensor) a.bm = expected > 128 ? 256 : 128;
-  else if (a.layout == kFp8Dense) a.bm = expected <= 16 ? 16 : expected <= 32 ? 32 : expected <= 64 ? 64 : 128;
-  else a.bm = expected <= 9 ? 16 : expected <= 20 ? 32 : expected <= 44 ? 64 : 128;  // experts above the mean fit too
-  const int64_t likely_units = a.layout == kFp8Dense ? (a.rows + a.bm - 1) / a.bm : a.E * ((expected + a.bm - 1) / a.bm);
+  const Plan plan = choose_plan(a, expected, flags);
+  const bool tensor = plan.tensor;
+  a.bm = plan.bm;
   cudaError_t err;
   if (a.layout != kFp8Dense) {
     const Fp8Workspace ws = fp8_workspace(a.rows, a.E);
@@ -94,15 +150,20 @@ chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices
     a.block_row0 = block_row0;
     a.sorted_ids = sorted_ids;
   }
-  err = tensor ? launch_fp8_tile(a, stream) : launch_fp8_stream(a, likely_units, stream);
+  err = tensor ? launch_fp8_tile(a, stream) : launch_fp8_stream(a, plan.split, stream);
   return err == cudaSuccess ? CHORD_OK : cuda_fail(err, tensor ? "FP8 tensor-core GEMM launch" : "FP8 streaming GEMM launch");
 }
 
-// One kernel for gate_up once its 256-row x 128-column tiles cover the CTA pairs; below, the
-// product of twice as many tiles (or the weight streaming) and a quantisation are faster.
-bool fused_gate_up(int64_t M, int I, int num_sms, int flags) {
+// Whether gate_up runs as one kernel (256-row x 128-column tiles), or as the product in FP32
+// and a quantisation: whichever is estimated to take less time. 4096 x 7168, in us, one kernel
+// and two: M=256 38.8, 28.9; M=512 39.9, 38.4; M=1024 41.0, 44.1; M=4096 149, 155.
+bool fused_gate_up(const Fp8Args& a, int flags) {
   if (flags & CHORD_FLAG_FORCE_STREAM) return false;
-  return (flags & CHORD_FLAG_FORCE_TENSOR) || (M + 255) / 256 * (I / kFp8Block) >= num_sms / 2;
+  if (flags & CHORD_FLAG_FORCE_TENSOR) return true;
+  const int64_t tiles = (a.rows + 255) / 256 * (a.N / 256), pairs = a.num_sms / 2;
+  const double fused = 3.0 + double((tiles + pairs - 1) / pairs) * (fp8_blocks(a.K) * 0.54 + 2.0);
+  const double quantise = 3.5 + double(a.rows) * a.N * 8 / 5e6;  // FP32 sums written and read
+  return fused < choose_plan(a, a.rows, flags).us + quantise;
 }
 
 chord_status_t quantize(const void* x, int dtype, int64_t ld, int64_t rows, int K, int silu, const int32_t* masked_m,
@@ -240,7 +301,7 @@ chord_status_t chord_fp8_gate_up(const uint8_t* xq, const float* xs, int64_t M, 
   if ((st = current_device(&num_sms)) != CHORD_OK) return st;
   if (M == 0) return CHORD_OK;
   Fp8Args a = product_args(xq, xs, M, H, w13, ws13, 1, 2 * I, q, workspace, flags, kFp8Dense, num_sms);
-  if (fused_gate_up(M, I, num_sms, flags)) {
+  if (fused_gate_up(a, flags)) {
     a.out_scales = scales;
     const cudaError_t err = launch_fp8_tile_gate_up(a, reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? CHORD_OK : cuda_fail(err, "FP8 gate_up launch");

@@ -1,4 +1,4 @@
-// fp8_stream.cu -- FP8 block-128 products for up to 128 rows of an expert: the weights stream
+// fp8_stream.cu -- FP8 block-128 products for few rows of an expert: the weights stream
 // through once.
 //
 //   out[m, n] = sum_kb s[m, kb] * P_kb[n, m],   P_kb = w[n, kb] . xq[m, kb],
@@ -6,7 +6,7 @@
 //
 // With few rows the product reads N*K weight bytes for 2*N*K*rows operations, so HBM bounds
 // it. The operands are swapped against fp8_tile.cu: a tile of 128 weight rows (one block of
-// the weight scales) is the M side of the MMA and TN = 16 to 128 activation rows the N side,
+// the weight scales) is the M side of the MMA and TN = 16, 32 or 64 activation rows the N side,
 // so a weight byte is fetched once for all of them and the MMA's size follows the rows.
 //
 //   warp 0      TMA producer: per k block 128 weight rows and TN activation rows, 128 bytes
@@ -35,22 +35,23 @@ constexpr int kWRows = 128;                     // weight rows of a tile
 constexpr int kWBytes = kWRows * kFp8Block;
 constexpr int kThreads = 256;
 constexpr int kFirstPromote = 4, kPromote = 4;  // warps
+constexpr int kMaxSplit = 8;                    // CTAs that may share an item (a portable cluster)
 constexpr int kGroupKb = 8;                     // k blocks of a scale group
 
 template <int TN>
 struct StreamCfg {
-  // TN <= 64: two CTAs share an SM (half the shared memory and tensor memory, 128 registers
-  // a thread), so one's start and end overlap the other's streaming
-  static constexpr int kCtas = TN <= 64 ? 2 : 1;
+  // two CTAs share an SM (half the shared memory and tensor memory, 128 registers a thread),
+  // so one's start and end overlap the other's streaming
+  static constexpr int kCtas = kFp8StreamCtas;
   static constexpr int kStageBytes = kWBytes + TN * kFp8Block;
   static constexpr int kGroups = 3;                               // scale groups in the ring
   static constexpr int kScaleBytes = kGroups * kGroupKb * TN * 4;
   static constexpr int kFixed = 1024 + kScaleBytes;
-  static constexpr int kBudget = (TN <= 64 ? 113 : 226) * 1024 - 1024;  // less alignment slack
+  static constexpr int kBudget = 113 * 1024 - 1024;  // less alignment slack
   static constexpr int kStages = (kBudget - kFixed) / kStageBytes;
   static constexpr int kSmem = 1024 + (kFixed + 1023) / 1024 * 1024 + kStages * kStageBytes;
   static constexpr int kBufs = 4;
-  static constexpr int kCols = kBufs * TN;                        // 64 .. 512, a power of two
+  static constexpr int kCols = kBufs * TN;                        // 64, 128 or 256
   static constexpr int kChunk = 16;
 };
 
@@ -58,9 +59,12 @@ struct StreamMaps {
   CUtensorMap x, w;
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -281,16 +285,30 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
     const int j_begin = int(rank) * TN / split, j_end = (int(rank) + 1) * TN / split;
     if (first < items && !abort_flag) {
       const int u = first / NT, n0 = (first - u * NT) * kWRows, row0 = unit_row0(u);
-      for (int i = threadIdx.x; i < (j_end - j_begin) * kWRows; i += kThreads) {
-        const int j = j_begin + i / kWRows, n = n0 + i % kWRows;
+      // four neighbouring columns a thread, every CTA's share requested before any is added
+      for (int i = threadIdx.x; i < (j_end - j_begin) * (kWRows / 4); i += kThreads) {
+        const int j = j_begin + i / (kWRows / 4), c0 = i % (kWRows / 4) * 4, n = n0 + c0;
         const bool live = p.layout == kFp8Dense ? row0 + j < p.rows : __ldg(p.sorted_ids + u * TN + j) >= 0;
-        if (!live || n >= p.N) continue;
-        const float* mine = partial + j * kWRows + i % kWRows;
-        float x = 0.f;
-        for (int c = 0; c < split; ++c) x += ld_cluster(cluster_addr(mine, c));
+        if (!live || n >= p.N) continue;  // N % 8 == 0: four columns are all in or all out
+        const float* mine = partial + j * kWRows + c0;
+        float4 part[kMaxSplit];
+#pragma unroll
+        for (int c = 0; c < kMaxSplit; ++c)
+          if (c < split) part[c] = ld_cluster4(cluster_addr(mine, c));
+        float4 x = part[0];
+#pragma unroll
+        for (int c = 1; c < kMaxSplit; ++c)
+          if (c < split) x.x += part[c].x, x.y += part[c].y, x.z += part[c].z, x.w += part[c].w;
         const int64_t at = int64_t(row0 + j) * p.N + n;
-        if (p.out_f32) static_cast<float*>(p.out)[at] = x;
-        else static_cast<uint16_t*>(p.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        if (p.out_f32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = x;
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+          uint2 v;
+          v.x = *reinterpret_cast<const uint32_t*>(&lo);
+          v.y = *reinterpret_cast<const uint32_t*>(&hi);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = v;
+        }
       }
     }
     __syncthreads();
@@ -303,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
 }
 
 template <int TN>
-cudaError_t launch(const Fp8Args& a, int64_t likely_units, cudaStream_t stream) {
+cudaError_t launch(const Fp8Args& a, int split, cudaStream_t stream) {
   using Cfg = StreamCfg<TN>;
   static_assert(Cfg::kStages >= 3 && Cfg::kStages * Cfg::kStageBytes >= TN * kWRows * 4, "ring");
   auto kern = fp8_stream_kernel<TN>;
@@ -313,15 +331,11 @@ cudaError_t launch(const Fp8Args& a, int64_t likely_units, cudaStream_t stream) 
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if ((err = matrix_map(&maps.x, u8, 1, a.xq, a.rows, a.K, TN)) != cudaSuccess) return err;
   if ((err = matrix_map(&maps.w, u8, 1, a.w, int64_t(a.E) * a.N, a.K, kWRows)) != cudaSuccess) return err;
-  const int64_t tiles = (a.N + kWRows - 1) / kWRows, KB = fp8_blocks(a.K);
+  const int64_t tiles = (a.N + kWRows - 1) / kWRows;
   // upper bound of the items (the grouped unit count is on the device)
   const int64_t items = ((a.rows + TN - 1) / TN + (a.layout == kFp8Dense ? 0 : a.E)) * tiles;
   if (items >= int64_t(1) << 28) return cudaErrorInvalidValue;
-  // CTAs that share an item: as many as keep the likely items within one wave, each with two
-  // k blocks at least
   const int64_t slots = int64_t(a.num_sms) * Cfg::kCtas;
-  int split = 1;
-  while (split < 8 && likely_units * tiles * split * 2 <= slots && KB >= 4 * split) split *= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -343,12 +357,11 @@ cudaError_t launch(const Fp8Args& a, int64_t likely_units, cudaStream_t stream) 
 
 }  // namespace
 
-cudaError_t launch_fp8_stream(const Fp8Args& a, int64_t likely_units, cudaStream_t stream) {
+cudaError_t launch_fp8_stream(const Fp8Args& a, int split, cudaStream_t stream) {
   switch (a.bm) {
-    case 16: return launch<16>(a, likely_units, stream);
-    case 32: return launch<32>(a, likely_units, stream);
-    case 64: return launch<64>(a, likely_units, stream);
-    default: return launch<128>(a, likely_units, stream);
+    case 16: return launch<16>(a, split, stream);
+    case 32: return launch<32>(a, split, stream);
+    default: return launch<64>(a, split, stream);
   }
 }
 
