@@ -51,6 +51,7 @@ _DTYPES = {torch.float32: CHORD_DTYPE_F32, torch.bfloat16: CHORD_DTYPE_BF16, tor
 CHORD_SCORE_SOFTMAX = 0
 CHORD_SCORE_SIGMOID = 1
 _FP8_TYPES = (torch.float8_e4m3fn, torch.uint8)
+_FP8_INPUTS = (torch.bfloat16, torch.float32)
 _SCORES = {"softmax": CHORD_SCORE_SOFTMAX, "sigmoid": CHORD_SCORE_SIGMOID}
 
 # every symbol include/chord.h declares: (name, restype, argtypes)
@@ -601,6 +602,9 @@ class ChordFP8MLP:
         self.H, self.I = w13.shape[1], w13.shape[0] // 2
         if tuple(w2.shape) != (self.H, self.I):
             raise ValueError(f"w2 has shape {tuple(w2.shape)}, w13 {tuple(w13.shape)}")
+        H, I = self.H, self.I
+        self._weights = (_fp8_codes(w13, "w13"), _fp8_scales(s13, "s13", (_blocks128(2 * I), _blocks128(H))),
+                         _fp8_codes(w2, "w2"), _fp8_scales(s2, "s2", (_blocks128(H), _blocks128(I))))
         self.device = w13.device
         self.max_tokens = -1
         self.reserve(max_tokens)
@@ -614,7 +618,8 @@ class ChordFP8MLP:
         need = max(chord_fp8_gate_up_workspace_bytes(T, self.I), chord_fp8_workspace_bytes(T, 1))
         self.workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=d)
         self.max_tokens = T
-        self.viewed, self.views = -1, None
+        self._pointers = (*self._weights, _ptr(self.xq), _ptr(self.xs), _ptr(self.aq), _ptr(self.as_),
+                          _ptr(self.workspace), _nbytes(self.workspace))
 
     def forward(self, x, out=None, flags=0):
         """out [T, H] (bf16, or the fp32 sums if an fp32 `out` is given) for bf16 or fp32 x [T, H]."""
@@ -625,14 +630,18 @@ class ChordFP8MLP:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         if T == 0:
             return out
-        if T != self.viewed:  # the buffers seen as T rows
-            self.views = (self.xq[:T * self.H].view(T, self.H), self.xs[:T * _blocks128(self.H)].view(-1, T),
-                          self.aq[:T * self.I].view(T, self.I), self.as_[:T * _blocks128(self.I)].view(-1, T))
-            self.viewed = T
-        xq, xs, aq, a_s = self.views
-        chord_fp8_quantize(x, xq, xs)
-        chord_fp8_gate_up(xq, xs, self.w13, self.s13, aq, a_s, self.workspace, flags)
-        chord_fp8_gemm(aq, a_s, self.w2, self.s2, out, self.workspace, flags)
+        # the layer's own tensors were checked when they were made: the three calls take their
+        # pointers as they are, only x and out are new
+        assert x.shape == (T, self.H) and x.dtype in _FP8_INPUTS, f"x must be bf16 or fp32 [T, {self.H}]"
+        x_ptr, x_ld = _rows_ptr(x)
+        out_ptr, down_flags = _fp8_out(out, T, self.H, flags)
+        w13, s13, w2, s2, xq, xs, aq, a_s, ws, ws_bytes = self._pointers
+        lib_, s = lib(), _stream()
+        _check(lib_.chord_fp8_quantize(x_ptr, _DTYPES[x.dtype], x_ld, T, self.H, None, 0, xq, xs, s), "chord_fp8_quantize")
+        _check(lib_.chord_fp8_gate_up(xq, xs, T, self.H, w13, s13, self.I, aq, a_s, ws, ws_bytes, flags, s),
+               "chord_fp8_gate_up")
+        _check(lib_.chord_fp8_gemm(aq, a_s, T, self.I, w2, s2, self.H, out_ptr, ws, ws_bytes, down_flags, s),
+               "chord_fp8_gemm")
         return out
 
     __call__ = forward

@@ -131,6 +131,7 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
 // The product by the schedule chosen for `expected` rows per expert.
 chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices, const int32_t* masked_m,
                            int64_t max_m, void* workspace, int flags, cudaStream_t stream) {
+  if (expected > a.rows) expected = a.rows;
   const Plan plan = choose_plan(a, expected, flags);
   const bool tensor = plan.tensor;
   a.bm = plan.bm;

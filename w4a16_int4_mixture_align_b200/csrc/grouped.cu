@@ -35,16 +35,8 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kBatch = 256;                    // contiguous chunks per pass
 constexpr int kPerWarp = kBatch / kRouteWarps;  // chunks a warp classifies per batch
 
-__device__ __forceinline__ int warp_min(int v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-__device__ __forceinline__ int warp_max(int v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
+__device__ __forceinline__ int warp_min(int v) { return __reduce_min_sync(0xffffffffu, v); }
+__device__ __forceinline__ int warp_max(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // Exclusive prefix sum of v over the threads of a 1024-thread block; every thread must
 // call it. Returns the sum over the threads before this one and writes the block total
@@ -99,6 +91,8 @@ __global__ void __launch_bounds__(kRouteThreads) grouped_route_masked_kernel(
   __shared__ int s_warp[33];
   __shared__ int s_base[kRouteThreads];
   __shared__ int s_rows[kRouteThreads];
+  grid_dep_wait();
+  grid_dep_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
   int cnt = 0, units = 0;
@@ -150,6 +144,8 @@ __global__ void __launch_bounds__(kRouteThreads) grouped_route_contiguous_kernel
   __shared__ int s_e[kBatch][2];             // expert of each block, -1 when it is skipped
   __shared__ int s_base[kBatch];             // first unit of each chunk
   __shared__ int s_warp[33];
+  grid_dep_wait();
+  grid_dep_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int U = bm == 256 ? 2 : 1;
   const int sb = bm < 128 ? bm : 128;  // rows per unit inside one block
@@ -158,8 +154,9 @@ __global__ void __launch_bounds__(kRouteThreads) grouped_route_contiguous_kernel
   bool bad = false;
 
   for (int64_t c0 = 0; c0 < n_chunks; c0 += kBatch) {
-    // ---- classify: warp w takes chunks w*kPerWarp .. +kPerWarp-1 of the batch, loading
-    // kLoadAhead chunks before reducing any (registers allow no more at 1024 threads)
+    // ---- classify: warp w takes chunks w, w + 32, ... of the batch (a short batch then still
+    // occupies every warp), loading kLoadAhead of them before reducing any (registers allow
+    // no more at 1024 threads)
     constexpr int kLoadAhead = 4;
 #pragma unroll 1
     for (int j0 = 0; j0 < kPerWarp; j0 += kLoadAhead) {
@@ -168,12 +165,13 @@ __global__ void __launch_bounds__(kRouteThreads) grouped_route_contiguous_kernel
       for (int j = 0; j < kLoadAhead; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t c = c0 + warp * kPerWarp + j0 + j;
+          const int64_t c = c0 + warp + (j0 + j) * kRouteWarps;
           v[j][h] = make_int4(-1, -1, -1, -1);
           if (h < U && c < n_chunks) v[j][h] = load_ids4(m_indices, (c * U + h) * 128 + 4 * lane, M);
         }
 #pragma unroll
-      for (int j = 0; j < kLoadAhead; ++j)
+      for (int j = 0; j < kLoadAhead; ++j) {
+        if (c0 + warp + (j0 + j) * kRouteWarps >= n_chunks) break;  // nothing reads its entries
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int4 q = v[j][h];
@@ -200,17 +198,18 @@ __global__ void __launch_bounds__(kRouteThreads) grouped_route_contiguous_kernel
           for (int w = 0; w < 4; ++w)
             word[w] = __reduce_or_sync(0xffffffffu, (lane >> 3) == w ? nib << (4 * (lane & 7)) : 0u);
           if (lane == 0) {
-            const int i = warp * kPerWarp + j0 + j;
+            const int i = warp + (j0 + j) * kRouteWarps;
 #pragma unroll
             for (int w = 0; w < 4; ++w) s_bits[i][h][w] = word[w];
             s_e[i][h] = e;
           }
         }
+      }
     }
     __syncthreads();
     // ---- units per chunk, numbered by a prefix sum
     int cnt = 0;
-    if (tid < kBatch) {
+    if (tid < kBatch && c0 + tid < n_chunks) {
       const int e0 = s_e[tid][0], e1 = s_e[tid][1];
       if (U == 2) {
         cnt = (e0 >= 0 && e0 == e1) ? 1 : int(e0 >= 0) + int(e1 >= 0);
@@ -313,15 +312,17 @@ GroupedWorkspace grouped_workspace(int64_t rows, int E) {
 cudaError_t launch_grouped_route(const int32_t* m_indices, int64_t M, const int32_t* masked_m, int E,
                                  int64_t max_m, int bm, int32_t* expert_ids, int32_t* block_row0,
                                  int32_t* sorted_ids, int32_t* ntp, uint32_t* status, cudaStream_t stream) {
+  cudaError_t err;
   if (masked_m) {
-    grouped_route_masked_kernel<<<1, kRouteThreads, 0, stream>>>(masked_m, E, max_m, bm, expert_ids, block_row0,
-                                                                 sorted_ids, ntp, status);
+    err = launch_pdl(true, grouped_route_masked_kernel, dim3(1), dim3(kRouteThreads), 0, stream, masked_m, E, max_m, bm,
+                     expert_ids, block_row0, sorted_ids, ntp, status);
   } else {
     const int U = bm == 256 ? 2 : 1;
     const int64_t n_chunks = ((M + 127) / 128 + U - 1) / U;
-    grouped_route_contiguous_kernel<<<1, kRouteThreads, 0, stream>>>(m_indices, M, E, bm, n_chunks, expert_ids,
-                                                                     block_row0, sorted_ids, ntp, status);
+    err = launch_pdl(true, grouped_route_contiguous_kernel, dim3(1), dim3(kRouteThreads), 0, stream, m_indices, M, E, bm,
+                     n_chunks, expert_ids, block_row0, sorted_ids, ntp, status);
   }
+  if (err != cudaSuccess) return err;
   count_launches(1);
   return cudaGetLastError();
 }
