@@ -76,9 +76,9 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [S]
-  uint64_t* empty = full + S;                          // [S]
-  uint64_t* acc_full = empty + S;                      // [B]
-  uint64_t* acc_empty = acc_full + B;                  // [B]
+  uint64_t* done = full + S;                           // [S] stage multiplied: it may be refilled, its
+                                                       // product read
+  uint64_t* acc_empty = done + S;                      // [B]
   uint64_t* sc_full = acc_empty + B;                   // [kGroups]
   uint64_t* sc_empty = sc_full + Cfg::kGroups;         // [kGroups]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_empty + Cfg::kGroups);
@@ -92,10 +92,9 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
     abort_flag = 0;
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&done[s], 1);
     }
     for (int b = 0; b < B; ++b) {
-      mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], kPromote);
     }
     for (int g = 0; g < Cfg::kGroups; ++g) {
@@ -131,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
         const int u = i / NT, row = unit_row0(u), wrow = unit_expert(u) * p.N + (i - u * NT) * kWRows;
         for (int kb = kb_begin; kb < kb_end; ++kb, ++fill) {
           const uint32_t s = fill % S;
-          if (fill >= S && !mbar_wait(&empty[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
+          if (fill >= S && !mbar_wait(&done[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
             ok = false;
             break;
           }
@@ -163,13 +162,12 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
           const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kWBytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_e4m3<1>(tmem + b * TN, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-          commit<1>(&empty[s]);
-          commit<1>(&acc_full[b]);
+          commit<1>(&done[s]);
         }
       }
       if (it > 0) {  // no MMA writes tensor memory once it is freed
         int dummy = 0;
-        mbar_wait(&empty[(it - 1) % S], ((it - 1) / S) & 1, &dummy, p.status);
+        mbar_wait(&done[(it - 1) % S], ((it - 1) / S) & 1, &dummy, p.status);
       }
     }
     __syncwarp();
@@ -216,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
         const int in_group = (kb - kb_begin) % kGroupKb;
         if (in_group == 0) ok = mbar_wait_warp(&sc_full[g], (grp / Cfg::kGroups) & 1, abort_v, p.status);
         const uint32_t b = it % B;
-        ok = ok && mbar_wait_warp(&acc_full[b], (it / B) & 1, abort_v, p.status);
+        ok = ok && mbar_wait_warp(&done[it % S], (it / S) & 1, abort_v, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sc = smem_u32(scales + (g * kGroupKb + in_group) * TN);

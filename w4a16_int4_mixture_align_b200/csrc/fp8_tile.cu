@@ -12,8 +12,9 @@
 //   warps 0, 2  TMA producers: per k block 128 activation rows (warp 0) and this CTA's
 //               weight rows (warp 2), 128 bytes wide (128-byte swizzle), into a ring of
 //               stages.
-//   warp 1      MMA issuer (one thread): four tcgen05.mma (K = 32) per k block, the first
-//               overwriting the buffer; commits free the stage and publish the buffer.
+//   warps 1, 3  MMA issuers (one thread each, for even and odd k blocks): four tcgen05.mma
+//               (K = 32) per k block, the first overwriting the buffer; a commit frees the
+//               stage and publishes the buffer.
 //   warps 4..11 promotion: tcgen05.ld of the buffer (four warps per 32-lane quadrant pair,
 //               each half of the columns), FP32 accumulation in registers, output.
 //
@@ -127,9 +128,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [S] stage loaded (rank 0's is used)
-  uint64_t* empty = full + S;                          // [S] stage consumed
-  uint64_t* acc_full = empty + S;                      // [2] buffer holds a k block's product
-  uint64_t* acc_empty = acc_full + 2;                  // [2] buffer read by every warp (rank 0's is used)
+  uint64_t* done = full + S;                           // [S] stage multiplied: it may be refilled, its
+                                                       // product read (one commit a block: each holds a
+                                                       // pair's MMAs up by about 400 cycles)
+  uint64_t* acc_empty = done + S;                      // [2] buffer read by every warp (rank 0's is used)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   __shared__ int abort_flag;
   // kGateUp: maxima of the rows by column half, in the half of a staging box it does not use
@@ -142,10 +144,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     abort_flag = 0;
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&done[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], kPromoteWarps * CG);
     }
     fence_barrier_init();
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           else row = (p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u)) * p.N + nt * BN + int(rank) * Cfg::kBRows;
           for (int kb = 0; kb < KB; ++kb, ++fill) {
             const uint32_t s = fill % S;
-            if (fill >= S && !mbar_wait(&empty[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
+            if (fill >= S && !mbar_wait(&done[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
               ok = false;
               break;
             }
@@ -203,35 +204,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    } else if (lane == 0 && rank == 0) {
+      // warp 1 multiplies the even k blocks, warp 3 the odd ones: issuing a block's MMAs holds
+      // its thread for about their time, so a single issuer's waits and commits between two
+      // blocks were time that the tensor core stood still
       constexpr uint32_t idesc = idesc_e4m3(kBM * CG, BN);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = cid; t < tiles && ok; t += ncl) {
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const uint32_t s = it % S, b = it & 1;
-          if ((it >= 2 && !mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1, abort_v, p.status)) ||
-              !mbar_wait(&full[s], (it / S) & 1, abort_v, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes;
-          const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kABytes);
+      const uint32_t b = warp == 1 ? 0 : 1;  // its tensor-memory buffer
+      const uint32_t blocks = uint32_t(cid < tiles ? (tiles - cid + ncl - 1) / ncl : 0) * uint32_t(KB);
+      uint32_t it = b;
+      for (; it < blocks; it += 2) {
+        const uint32_t s = it % S;
+        if ((it >= 2 && !mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1, abort_v, p.status)) ||
+            !mbar_wait(&full[s], (it / S) & 1, abort_v, p.status))
+          break;
+        tc_fence_after();
+        const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes;
+        const uint64_t ad = sw128_kmajor_desc(st), bd = sw128_kmajor_desc(st + kABytes);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_e4m3<CG>(tmem + b * BN, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-          commit<CG>(&empty[s]);
-          commit<CG>(&acc_full[b]);
-        }
+        for (int k = 0; k < 4; ++k) mma_e4m3<CG>(tmem + b * BN, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+        commit<CG>(&done[s]);
       }
-      if (it > 0) {  // no MMA writes tensor memory once it is freed
+      if (it >= 2) {  // no MMA writes tensor memory once it is freed
         int dummy = 0;
-        mbar_wait(&empty[(it - 1) % S], ((it - 1) / S) & 1, &dummy, p.status);
+        mbar_wait(&done[(it - 2) % S], ((it - 2) / S) & 1, &dummy, p.status);
       }
     }
     __syncwarp();
-    }
   } else {
     take_registers<232>();
     const int q = warp & 3;            // the tensor-memory lanes this warp may read
@@ -273,7 +271,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // blocks too
       constexpr int W = kChunkCols, CH = COLS / W;
       uint32_t v[2][W];
-      ok = mbar_wait_warp(&acc_full[it & 1], (it >> 1) & 1, abort_v, p.status);
+      ok = mbar_wait_warp(&done[it % S], (it / S) & 1, abort_v, p.status);
       tc_fence_after();
       tmem_ld_async(src + (it & 1) * BN, v[0]);
 #pragma unroll 1
@@ -302,7 +300,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               if (CG == 2) mbar_arrive_cluster(empty0 + b * 8);
               else mbar_arrive(&acc_empty[b]);
             }
-            if (kb + 1 < KB) ok = ok && mbar_wait_warp(&acc_full[it & 1], (it >> 1) & 1, abort_v, p.status);
+            if (kb + 1 < KB) ok = ok && mbar_wait_warp(&done[it % S], (it / S) & 1, abort_v, p.status);
             tc_fence_after();
             // after the last block this rereads a buffer of this CTA, for nothing
             tmem_ld_async(src + (it & 1) * BN, v[0]);
