@@ -83,6 +83,7 @@ int stream_split(int64_t items, int KB, int64_t slots) {
 struct Plan {
   bool tensor;  // the tile kernel (fp8_tile.cu) or the streaming one (fp8_stream.cu)
   int bm;       // rows of a unit
+  int bn;       // columns of a tile
   int split;    // streaming: CTAs that share an item
   double us;    // estimate
 };
@@ -91,8 +92,9 @@ struct Plan {
 // wave of the CTAs, the k blocks of an item times a time per block (and a time per tile),
 // fitted to measurements on a B200 over M = 8 .. 4096 of 4096 x 7168, 7168 x 2048, 512 x 7168,
 // 576 x 1520 and 7168 x 256 (N x K); it lies within a quarter of them. On both sides of some
-// borders, in us: 4096 x 7168 M=128 64-row streaming 14.0, 128-row tiles 27.4, 256-row 32.2;
-// M=384 35.7, 28.9, 32.8; M=768 -, 52.3, 33.6; 512 x 7168 M=512 11.5, 27.3, 31.5.
+// borders, in us, for 64-row streaming, 128 x 128, 128 x 256 and 256 x 256 tiles: 4096 x 7168
+// M=128 14.0, 19.7, 29.3, 29.8; M=384 35.7, 21.4, 30.1, 31.3; M=768 -, 37.6, 32.5, 32.5; M=4096
+// -, 175, 122, 121; 512 x 7168 M=512 11.5, 19.5, 29.1, 29.1; 7168 x 2048 M=384 23, 14.2, 13.2, 13.4.
 // `expected`: rows per expert; grouped experts are taken to hold up to 1.25 times as many, and
 // contiguous ones whole 128-row blocks.
 Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
@@ -105,8 +107,8 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
   auto waves = [](int64_t items, int64_t slots) { return double((items + slots - 1) / slots); };
   Plan best{};
   best.us = 1e30;
-  auto offer = [&](bool tensor, int bm, int split, double us) {
-    if (us < best.us) best = Plan{tensor, bm, split, us};
+  auto offer = [&](bool tensor, int bm, int bn, int split, double us) {
+    if (us < best.us) best = Plan{tensor, bm, bn, split, us};
   };
   if (!(flags & CHORD_FLAG_FORCE_TENSOR)) {
     const double start[3] = {4.6, 5.0, 6.4}, per_kb[3] = {0.37, 0.39, 0.52};
@@ -118,12 +120,13 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
       // a split grid covers every unit there may be, so it has to stay small
       const int64_t most = ((a.rows + bm - 1) / bm + (a.layout == kFp8Dense ? 0 : a.E)) * tiles;
       if (most * split > 8 * slots) split = 1;
-      offer(false, bm, split, start[i] + waves(items * split, slots) * ((KB + split - 1) / split) * per_kb[i]);
+      offer(false, bm, 128, split, start[i] + waves(items * split, slots) * ((KB + split - 1) / split) * per_kb[i]);
     }
   }
   if (!(flags & CHORD_FLAG_FORCE_STREAM)) {
-    offer(true, 128, 1, 2.4 + waves(units_of(128) * ((a.N + 127) / 128), a.num_sms) * (KB * 0.42 + 1.2));
-    offer(true, 256, 1, 3.0 + waves(units_of(256) * ((a.N + 255) / 256), a.num_sms / 2) * (KB * 0.54 + 0.9));
+    offer(true, 128, 128, 1, 2.6 + waves(units_of(128) * ((a.N + 127) / 128), a.num_sms) * (KB * 0.31 + 1.2));
+    offer(true, 256, 256, 1, 3.0 + waves(units_of(256) * ((a.N + 255) / 256), a.num_sms / 2) * (KB * 0.50 + 0.9));
+    offer(true, 128, 256, 1, 3.0 + waves(units_of(128) * ((a.N + 255) / 256), a.num_sms) * (KB * 0.50 + 0.9));
   }
   return best;
 }
@@ -135,6 +138,7 @@ chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices
   const Plan plan = choose_plan(a, expected, flags);
   const bool tensor = plan.tensor;
   a.bm = plan.bm;
+  a.bn = plan.bn;
   cudaError_t err;
   if (a.layout != kFp8Dense) {
     const Fp8Workspace ws = fp8_workspace(a.rows, a.E);
@@ -162,7 +166,7 @@ bool fused_gate_up(const Fp8Args& a, int flags) {
   if (flags & CHORD_FLAG_FORCE_STREAM) return false;
   if (flags & CHORD_FLAG_FORCE_TENSOR) return true;
   const int64_t tiles = (a.rows + 255) / 256 * (a.N / 256), pairs = a.num_sms / 2;
-  const double fused = 3.0 + double((tiles + pairs - 1) / pairs) * (fp8_blocks(a.K) * 0.54 + 2.0);
+  const double fused = 3.0 + double((tiles + pairs - 1) / pairs) * (fp8_blocks(a.K) * 0.50 + 2.0);
   const double quantise = 3.5 + double(a.rows) * a.N * 8 / 5e6;  // FP32 sums written and read
   return fused < choose_plan(a, a.rows, flags).us + quantise;
 }

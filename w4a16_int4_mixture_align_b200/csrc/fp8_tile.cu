@@ -19,11 +19,16 @@
 //               each half of the columns), FP32 accumulation in registers, output.
 //
 // CG = 2 runs a CTA pair (cta_group::2): M = 256, each CTA holding 128 activation rows and
-// half of the weight rows, so a CTA fetches 32 KiB per 256 x 256 x 128 step instead of 48:
-// at full rate 128 x 256 tiles of single CTAs would ask L2 for half as much again.
+// half of the weight rows, so a CTA fetches 32 KiB per 256 x 256 x 128 step instead of the 48
+// of a single 128 x 256 tile. At 8192 x 4096 x 7168 (M x N x K) the pairs take 220 us and the
+// single tiles 228, at 4096 rows 121 and 122; the single ones serve units of 128 rows. 128 x
+// 128 tiles serve products of few tiles (512 rows: 21 us against 31).
 //
-// Per k block of a 128 x 256 CTA tile the MMA takes 512 cycles (8192 FP8 multiply-adds a
-// cycle), the promotion 256 cycles of the FP32 pipe: the tensor core stays the bound.
+// Bound: the round trip of a tensor-memory buffer. Measured in cycles, a block's MMAs take
+// 660 (an instruction of K = 32 takes 130 to 165 whatever its N), their end is seen 340
+// later, reading the buffer takes 440 and handing it back 500; with two buffers that is about
+// 1000 a block, 2.2 PFLOP/s. The TMA feed alone would allow 660 (3.2 PFLOP/s while operands
+// stay in L2), the FP32 additions 256.
 //
 // All waits are bounded. On a timeout a CTA raises CHORD_DEV_TIMEOUT, waits (bounded) for
 // its copies and MMAs in flight, frees its tensor memory and returns.
@@ -214,8 +219,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint32_t it = b;
       for (; it < blocks; it += 2) {
         const uint32_t s = it % S;
-        if ((it >= 2 && !mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1, abort_v, p.status)) ||
-            !mbar_wait(&full[s], (it / S) & 1, abort_v, p.status))
+        if (!mbar_wait(&full[s], (it / S) & 1, abort_v, p.status) ||
+            (it >= 2 && !mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1, abort_v, p.status)))
           break;
         tc_fence_after();
         const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes;
@@ -446,7 +451,8 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream) {
-  return a.bm == 256 ? launch<2, 256, kRows>(a, stream) : launch<1, 128, kRows>(a, stream);
+  if (a.bm == 256) return launch<2, 256, kRows>(a, stream);
+  return a.bn == 256 ? launch<1, 256, kRows>(a, stream) : launch<1, 128, kRows>(a, stream);
 }
 
 cudaError_t launch_fp8_tile_gate_up(const Fp8Args& a, cudaStream_t stream) {
