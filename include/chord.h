@@ -355,10 +355,11 @@ CHORD_API chord_status_t chord_grouped_masked(const uint16_t* x, int E, int64_t 
  *               xq[m, k] * w[e_m][n, k])
  * All sums are FP32 (the inner one in the tensor core, at most 128 exact products); out is
  * bf16, rounded once, or with CHORD_FLAG_OUTPUT_FP32 the FP32 sums (a tensor-parallel
- * rank's partial). The result of a row depends on neither the other rows nor the call.
+ * rank's partial). A row's result depends on the shapes and flags of the call, not on the
+ * other rows, and is the same call after call.
  *
  * Requires K % 16 == 0, N % 8 == 0, xq, w and out 16-byte aligned, xs and ws 4-byte
- * aligned, rows < 2^31 - 256, 1 <= E <= 1024. Every element of out that belongs to a row of
+ * aligned, rows < 2^30, 1 <= E <= 1024, E * N < 2^31. Every element of out that belongs to a row of
  * some expert is written, and no other.
  *
  * chord_fp8_gemm: one matrix (E = 1), every row. w [N, K], ws [ceil(N/128), ceil(K/128)].

@@ -406,3 +406,75 @@ def test_graph_replay_on_another_stream(chord):
         torch.cuda.synchronize()
         got = out.clone()
         assert torch.equal(got, mlp(x, out=out))
+
+
+def test_masked_quantise_takes_expert_batches(chord):
+    """[E, max_m, K] tensors as they are; a transposed code tensor is refused, not lost."""
+    import torch
+    x = torch.randn((3, 4, 256), device="cuda", dtype=torch.float32)
+    q = torch.zeros((3, 4, 256), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((2, 12), device="cuda")
+    m = torch.tensor([4, 4, 4], dtype=torch.int32, device="cuda")
+    chord.chord_fp8_quantize(x, q, s, masked_m=m)
+    check_quantised(q.view(12, 256).cpu().numpy(), s.cpu().numpy(), x.view(12, 256).cpu().numpy())
+    with pytest.raises(AssertionError):
+        chord.chord_fp8_quantize(x, q.transpose(0, 1), s, masked_m=m)
+    with pytest.raises(RuntimeError):
+        chord.chord_fp8_quantize(x.transpose(0, 1), q, s, masked_m=m)
+
+
+def test_graph_outlives_a_larger_call(chord):
+    """A graph captured before the MLP's buffers grew replays on the ones it was captured with."""
+    import torch
+    H, I = 256, 128
+    mlp = chord.ChordFP8MLP(*[cuda(v) for v in (codes((2 * I, H), 5), scales((2, 2), 7), codes((H, I), 6),
+                                                scales((2, 1), 8))], max_tokens=4)
+    x = torch.randn((4, H), device="cuda").to(torch.bfloat16)
+    want = mlp(x).clone()
+    out = torch.empty((4, H), dtype=torch.bfloat16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mlp(x, out=out)
+    mlp(torch.randn((300, H), device="cuda").to(torch.bfloat16))
+    junk = [torch.full((1 << 20,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    del junk
+
+
+def test_two_streams_at_once(chord):
+    """Products with workspaces of their own on two streams give what they give alone."""
+    import torch
+    jobs = []
+    for M, N, K, schedule in ((5, 512, 2048, "stream"), (300, 520, 1024, "tensor"), (64, 256, 4096, "auto")):
+        a = [cuda(v) for v in (codes((M, K), M), scales((-(-K // B), M), 1), codes((N, K), N), scales((-(-N // B), -(-K // B)), 2))]
+        w = workspace(chord, M)
+        ref = torch.empty((M, N), device="cuda")
+        chord.chord_fp8_gemm(*a, ref, w, flag(chord, schedule))
+        jobs.append((a, ref, torch.empty_like(ref), w, flag(chord, schedule), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, _, out, w, f, s in jobs:
+            with torch.cuda.stream(s):
+                chord.chord_fp8_gemm(*a, out, w, f)
+    torch.cuda.synchronize()
+    for _, ref, out, w, _, _ in jobs:
+        assert torch.equal(ref, out) and chord.chord_moe_check_status(w) == 0
+
+
+def test_far_rows(chord):
+    """Offsets beyond 2^31 bytes: the last rows of an activation matrix of 2.3 GB."""
+    import torch
+    rows, K, N = 150016, 16000, 8
+    xq = torch.zeros((rows, K), dtype=torch.uint8, device="cuda")
+    xs = torch.ones((-(-K // B), rows), device="cuda")
+    tail = codes((16, K), 3)
+    xq[-16:] = cuda(tail)
+    wq, ws = codes((N, K), 4), scales((1, -(-K // B)), 5)
+    y, a = ref64.product(tail, np.ones((-(-K // B), 16), np.float32), wq, ws)
+    for schedule in ("stream", "tensor"):
+        out = torch.full((rows, N), -7.0, device="cuda")
+        chord.chord_fp8_gemm(xq, xs, cuda(wq), cuda(ws), out, workspace(chord, rows), flag(chord, schedule))
+        check_rows(out, y, a, K, slice(rows - 16, rows))
+        assert (out[:-16] == 0).all()

@@ -150,6 +150,14 @@ def _rows_ptr(t):
     return t.data_ptr(), step
 
 
+def _here(*tensors):
+    """The work runs on the current device: the tensors (or None) have to be there too."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise AssertionError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
 def _typed(t, dtype, what, numel=None):
     """`t` (or None) after a check of its type and, if given, its number of elements."""
     assert t is None or t.dtype == dtype, f"{what} must be {dtype}, not {t.dtype}"
@@ -161,7 +169,7 @@ def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
     # the handle alone: torch.cuda.current_stream() builds an object, which takes 3 us
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _nbytes(t) -> int:
@@ -253,6 +261,7 @@ def chord_router_scored_align(logits, topk, E, block_m, topk_ids, topk_weights, 
     assert logits.dtype in _DTYPES, f"logits must be fp32, bf16 or fp16, not {logits.dtype}"
     T, G = logits.shape
     ptr, ld = _rows_ptr(logits)
+    _here(logits, bias, topk_ids, topk_weights, sorted_ids, expert_ids, num_tokens_padded, expert_offsets, workspace)
     _typed(topk_ids, torch.int32, "topk_ids", T * topk)
     _typed(topk_weights, torch.float32, "topk_weights", T * topk)
     _typed(bias, torch.float32, "bias", G)
@@ -348,15 +357,17 @@ def chord_fp8_gate_up_workspace_bytes(M, I) -> int:
 
 
 def _fp8_quantize(name, x, q, scales, masked_m, width, stream):
-    x2 = x.flatten(0, 1) if x.dim() == 3 else x  # [E, max_m, K] of the masked layout
-    q2 = q.flatten(0, 1) if q.dim() == 3 else q
-    rows, K = q2.shape
-    assert x2.shape == (rows, width * K), f"input has shape {tuple(x2.shape)}, codes {tuple(q2.shape)}"
-    assert x.dtype in (torch.bfloat16, torch.float32), f"input must be bf16 or fp32, not {x.dtype}"
+    codes = _fp8_codes(q, "q")
+    K = q.shape[-1]
+    rows = q.numel() // K if K else 0
+    x2 = x.view(-1, x.shape[-1]) if x.dim() == 3 else x  # [E, max_m, K] of the masked layout
+    assert x2.shape == (rows, width * K), f"input has shape {tuple(x.shape)}, codes {tuple(q.shape)}"
+    assert x.dtype in _FP8_INPUTS, f"input must be bf16 or fp32, not {x.dtype}"
     ptr, ld = _rows_ptr(x2)
     _typed(masked_m, torch.int32, "masked_m")
+    _here(x, q, scales, masked_m)
     _check(getattr(lib(), name)(ptr, _DTYPES[x.dtype], ld, rows, K, _ptr(masked_m),
-                                0 if masked_m is None else masked_m.numel(), _fp8_codes(q2, "q"),
+                                0 if masked_m is None else masked_m.numel(), codes,
                                 _fp8_scales(scales, "scales", (_blocks128(K), rows)), _stream(stream)), name)
 
 
@@ -375,6 +386,7 @@ def chord_fp8_gemm(xq, xs, w, ws, out, workspace, flags=0, stream=None):
     M, K = xq.shape
     N = w.shape[0]
     po, flags = _fp8_out(out, M, N, flags)
+    _here(xq, xs, w, ws, out, workspace)
     _check(lib().chord_fp8_gemm(_fp8_codes(xq, "xq"), _fp8_scales(xs, "xs", (_blocks128(K), M)), M, K,
                                 _fp8_codes(w, "w", (N, K)), _fp8_scales(ws, "ws", (_blocks128(N), _blocks128(K))), N,
                                 po, _ptr(workspace), _nbytes(workspace), flags, _stream(stream)), "chord_fp8_gemm")
@@ -386,6 +398,7 @@ def chord_fp8_grouped_contiguous(xq, xs, m_indices, w, ws, out, workspace, flags
     E, N, _ = w.shape
     po, flags = _fp8_out(out, M, N, flags)
     _typed(m_indices, torch.int32, "m_indices", M)
+    _here(xq, xs, m_indices, w, ws, out, workspace)
     _check(lib().chord_fp8_grouped_contiguous(
         _fp8_codes(xq, "xq"), _fp8_scales(xs, "xs", (_blocks128(K), M)), M, K, _ptr(m_indices),
         _fp8_codes(w, "w", (E, N, K)), _fp8_scales(ws, "ws", (E, _blocks128(N), _blocks128(K))), E, N, po,
@@ -396,13 +409,15 @@ def chord_fp8_grouped_masked(xq, xs, masked_m, expected_m, w, ws, out, workspace
     """The grouped product over a fixed row budget per expert (layout of chord_grouped_masked);
     xq is [E, max_m, K] or [E * max_m, K], out [E * max_m, N]."""
     E, N, K = w.shape
-    x2 = xq.flatten(0, 1) if xq.dim() == 3 else xq
-    rows = x2.shape[0]
+    rows = xq.numel() // K if K else 0
+    x_ptr = _fp8_codes(xq, "xq")
+    assert xq.shape[-1] == K, f"xq has {xq.shape[-1]} columns, w {K}"
     assert masked_m.numel() == E and rows % E == 0, f"{rows} rows and {masked_m.numel()} counts for {E} experts"
     po, flags = _fp8_out(out, rows, N, flags)
     _typed(masked_m, torch.int32, "masked_m")
+    _here(xq, xs, masked_m, w, ws, out, workspace)
     _check(lib().chord_fp8_grouped_masked(
-        _fp8_codes(x2, "xq", (rows, K)), _fp8_scales(xs, "xs", (_blocks128(K), rows)), E, rows // E, K,
+        x_ptr, _fp8_scales(xs, "xs", (_blocks128(K), rows)), E, rows // E, K,
         _ptr(masked_m), int(expected_m), _fp8_codes(w, "w"),
         _fp8_scales(ws, "ws", (E, _blocks128(N), _blocks128(K))), N, po, _ptr(workspace), _nbytes(workspace), flags,
         _stream(stream)), "chord_fp8_grouped_masked")
@@ -413,6 +428,7 @@ def chord_fp8_gate_up(xq, xs, w13, ws13, q, scales, workspace, flags=0, stream=N
     w13 [2 I, H]^T."""
     M, H = xq.shape
     I2 = w13.shape[0]
+    _here(xq, xs, w13, ws13, q, scales, workspace)
     _check(lib().chord_fp8_gate_up(
         _fp8_codes(xq, "xq"), _fp8_scales(xs, "xs", (_blocks128(H), M)), M, H, _fp8_codes(w13, "w13", (I2, H)),
         _fp8_scales(ws13, "ws13", (_blocks128(I2), _blocks128(H))), I2 // 2, _fp8_codes(q, "q", (M, I2 // 2)),
@@ -594,7 +610,8 @@ class ChordFP8MLP:
 
     w13 e4m3 [2 I, H] (gate rows first) with scales fp32 [2 I/128, H/128], w2 e4m3 [H, I] with
     scales [H/128, I/128]; the tensors are kept as they are. Buffers are sized for up to
-    ``max_tokens`` tokens; call with any T <= max_tokens.
+    ``max_tokens`` tokens and grow with a larger call. Calls (and replays of graphs) of one
+    layer share them, so they must not overlap on the GPU.
     """
 
     def __init__(self, w13, s13, w2, s2, max_tokens=1):
@@ -611,6 +628,9 @@ class ChordFP8MLP:
 
     def reserve(self, T: int):
         d = self.device
+        # a captured graph may still point to smaller buffers: they live as long as the layer
+        self._kept = getattr(self, "_kept", []) + ([self.xq, self.xs, self.aq, self.as_, self.workspace]
+                                                   if self.max_tokens >= 0 else [])
         self.xq = _alloc_bytes(T * self.H, d)
         self.xs = torch.empty(max(T * _blocks128(self.H), 1), dtype=torch.float32, device=d)
         self.aq = _alloc_bytes(T * self.I, d)
@@ -635,6 +655,7 @@ class ChordFP8MLP:
         assert x.shape == (T, self.H) and x.dtype in _FP8_INPUTS, f"x must be bf16 or fp32 [T, {self.H}]"
         x_ptr, x_ld = _rows_ptr(x)
         out_ptr, down_flags = _fp8_out(out, T, self.H, flags)
+        _here(x, out, self.w13)
         w13, s13, w2, s2, xq, xs, aq, a_s, ws, ws_bytes = self._pointers
         lib_, s = lib(), _stream()
         _check(lib_.chord_fp8_quantize(x_ptr, _DTYPES[x.dtype], x_ld, T, self.H, None, 0, xq, xs, s), "chord_fp8_quantize")

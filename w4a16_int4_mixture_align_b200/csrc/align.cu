@@ -13,8 +13,6 @@
 //
 //   n <= 4 x 1024  : one CTA of 32 warps (runs of ceil(n/1024) steps) does count, scan,
 //                    scatter and fill (1 launch)
-//   n <= 2^18      : a cluster of eight such CTAs, whose counts meet in distributed shared
-//                    memory (1 launch)
 //   larger n       : count kernel (per-chunk histograms) -> scan kernel (1 CTA) ->
 //                    scatter + fill kernel, histograms in the caller's workspace. A chunk
 //                    (one warp's run) is 256 slots, so a prefill batch spreads over
@@ -38,12 +36,10 @@ __host__ __device__ inline int multi_chunk(int64_t n, int E) {
   const int64_t g = (n + kChunkSmall - 1) / kChunkSmall;
   return int64_t(E) * g <= kMaxHistEntries ? kChunkSmall : kChunk;
 }
-// Up to this many 1024-slot chunks the routing sort runs in one CTA; above it, one cluster
-// sorts up to kClusterMaxSlots slots, and more go to the count / scan / scatter kernels (one
-// CTA sorting 32 chunks took ~70 us).
+// Up to this many 1024-slot chunks the routing sort runs in one CTA (one launch); above
+// it the count / scan / scatter kernels spread the slots over the GPU (one CTA sorting
+// 32 chunks took ~70 us).
 constexpr int kSingleMaxChunks = 4;
-constexpr int kSortCtas = 8;
-constexpr int64_t kClusterMaxSlots = int64_t(kSortCtas) * 32 * 32 * 32;  // 32 steps a warp
 
 // Loads the ids of `steps` (<= kSteps) 32-slot steps starting at c0, all up front so the
 // loads overlap; slots past n read as -1 (not local).
@@ -92,6 +88,7 @@ __device__ __forceinline__ void chunk_scatter(const int v[kSteps], int steps, in
   }
 }
 
+
 // Sentinel fill and expert_ids, shared by both paths.
 // cnt[e] = local slots, off[0..E] = padded offsets. Work items are distributed over
 // `worker` in [0, nworkers) threads.
@@ -121,43 +118,61 @@ __device__ void fill_tail(const int* cnt, const int* off, int E, int block_m, in
   }
 }
 
-template <int C, int MAXS>
-__global__ void __launch_bounds__(1024) align_cluster_kernel(
-    const int32_t* ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
-    int32_t* expert_ids, int32_t* ntp_out, int32_t* offsets_out) {
-  extern __shared__ int smem[];
-  grid_dep_wait();
-  grid_dep_trigger();
-  const int rank = C > 1 ? int(cluster_rank()) : 0;
-  align_body<C, 32, MAXS>(ids, n, n * rank / C, n * (rank + 1) / C, rank, E, block_m, cap, nblocks, sorted_ids,
-                          expert_ids, ntp_out, offsets_out, smem);
+// ---- single CTA (n <= kSingleMaxChunks chunks) ---------------------------------------
+// The whole sort by one CTA of 1024 threads; `smem` holds (32 + 2) * E + 34 ints.
+__device__ __forceinline__ void align_single_body(
+    const int32_t* __restrict__ ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks,
+    int32_t* __restrict__ sorted_ids, int32_t* __restrict__ expert_ids, int32_t* __restrict__ ntp_out,
+    int32_t* __restrict__ offsets_out, int* smem) {
+  int* hist = smem;                 // [32][E]
+  int* cnt = hist + 32 * E;         // [E]
+  int* off = cnt + E;               // [E+1]
+  int* wsum = off + E + 1;          // [33]
+  const int tid = threadIdx.x, warp = tid >> 5;
+  for (int i = tid; i < 32 * E; i += blockDim.x) hist[i] = 0;
+  __syncthreads();
+
+  // warp w owns `steps` consecutive 32-slot steps, so every warp works even for small n
+  const int nbits = key_bits(E);
+  const int steps = int((n + 32 * 32 - 1) / (32 * 32));
+  const int64_t c0 = int64_t(warp) * steps * 32;
+  int v[kSteps];
+  load_steps(ids, n, c0, steps, v);
+  if (c0 < n) chunk_count(v, steps, E, nbits, hist + warp * E);
+  __syncthreads();
+
+  for (int e = tid; e < E; e += blockDim.x) {
+    int run = 0;
+    for (int w = 0; w < 32; ++w) {
+      int c = hist[w * E + e];
+      hist[w * E + e] = run;
+      run += c;
+    }
+    cnt[e] = run;
+    off[e] = (run + block_m - 1) / block_m * block_m;
+  }
+  __syncthreads();
+  const int total = block_exclusive_scan(off, E, wsum);
+  if (tid == 0) off[E] = total;
+  for (int i = tid; i < 32 * E; i += blockDim.x) hist[i] += off[i % E];
+  __syncthreads();
+
+  if (c0 < n) chunk_scatter(v, steps, c0, E, nbits, hist + warp * E, sorted_ids);
+  fill_tail(cnt, off, E, block_m, n, cap, nblocks, sorted_ids, expert_ids, tid, blockDim.x);
+  if (tid == 0) {
+    ntp_out[0] = off[E];
+    ntp_out[1] = routing_tag(block_m);
+  }
+  if (offsets_out)
+    for (int e = tid; e <= E; e += blockDim.x) offsets_out[e] = off[e];
 }
 
-template <int C, int MAXS>
-cudaError_t launch_cluster(const int32_t* ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks,
-                           int32_t* sorted_ids, int32_t* expert_ids, int32_t* ntp, int32_t* offsets,
-                           cudaStream_t stream) {
-  auto kern = align_cluster_kernel<C, MAXS>;
-  const size_t smem = align_smem_bytes<32>(E);
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(C);
-  cfg.blockDim = dim3(1024);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, kern, ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets);
-  count_launches(1);
-  return err != cudaSuccess ? err : cudaGetLastError();
+__global__ void __launch_bounds__(1024) align_single_kernel(
+    const int32_t* __restrict__ ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks,
+    int32_t* __restrict__ sorted_ids, int32_t* __restrict__ expert_ids, int32_t* __restrict__ ntp_out,
+    int32_t* __restrict__ offsets_out) {
+  extern __shared__ int smem[];
+  align_single_body(ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp_out, offsets_out, smem);
 }
 
 // ---- router: top-k softmax routing, one warp per token ------------------------------
@@ -278,8 +293,8 @@ __global__ void __launch_bounds__(1024) router_align_single_kernel(
   extern __shared__ int smem[];
   route_tokens_any(logits, T, G, k, topk_ids, topk_weights, threadIdx.x >> 5, blockDim.x >> 5, threadIdx.x & 31);
   __syncthreads();
-  align_body<1, 32, 1>(topk_ids, T * k, 0, T * k, 0, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp_out,
-                       offsets_out, smem);
+  align_single_body(topk_ids, T * k, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp_out, offsets_out,
+                    smem);
 }
 
 
@@ -394,13 +409,16 @@ size_t align_workspace_bytes(int64_t n, int E) {
 cudaError_t launch_align(const int32_t* ids, int64_t n, int E, int block_m, int64_t cap,
                          int64_t nblocks, int32_t* sorted_ids, int32_t* expert_ids, int32_t* ntp,
                          int32_t* offsets, void* workspace, cudaStream_t stream) {
-  if ((n + kChunk - 1) / kChunk <= kSingleMaxChunks)
-    return launch_cluster<1, kSingleMaxChunks>(ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets,
-                                               stream);
-  if (n <= int64_t(kSortCtas) * 32 * 32 * 8)
-    return launch_cluster<kSortCtas, 8>(ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
-  if (n <= kClusterMaxSlots)
-    return launch_cluster<kSortCtas, 32>(ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
+  if ((n + kChunk - 1) / kChunk <= kSingleMaxChunks) {
+    const size_t smem = (size_t(32) * E + E + E + 1 + 33) * sizeof(int);
+    cudaError_t err = cudaFuncSetAttribute(align_single_kernel,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (err != cudaSuccess) return err;
+    align_single_kernel<<<1, 1024, smem, stream>>>(ids, n, E, block_m, cap, nblocks, sorted_ids,
+                                                   expert_ids, ntp, offsets);
+    count_launches(1);
+    return cudaGetLastError();
+  }
   const int csz = multi_chunk(n, E);
   const int64_t G = (n + csz - 1) / csz;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -431,7 +449,7 @@ cudaError_t launch_router_align(const float* logits, int64_t T, int G, int k, in
   const int64_t n = T * k;
   const int64_t G_chunks = (n + kChunk - 1) / kChunk;
   if (T <= kFusedMaxTokens && G_chunks <= kSingleMaxChunks) {
-    const size_t smem = align_smem_bytes<32>(E);
+    const size_t smem = (size_t(32) * E + E + E + 1 + 33) * sizeof(int);
     cudaError_t err = cudaFuncSetAttribute(router_align_single_kernel,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (err != cudaSuccess) return err;

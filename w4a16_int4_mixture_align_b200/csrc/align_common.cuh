@@ -1,6 +1,6 @@
-// align_common.cuh -- the block-padded routing sort by one CTA or one cluster, shared by the
-// sort kernels and the routers that sort in the same launch. The method is described in
-// align.cu.
+// align_common.cuh -- pieces of the block-padded routing sort: what align.cu and router.cu
+// share, and the sort by one CTA or one cluster with which the scored router ends. The
+// tensors and the method are described in align.cu.
 #pragma once
 
 #include "chord_internal.cuh"

@@ -35,6 +35,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/chord.h"
 
 namespace chord {
@@ -377,6 +379,21 @@ cudaError_t launch_pdl(bool pdl, void (*kernel)(Params...), dim3 grid, dim3 bloc
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Lets `kernel` use up to `bytes` of dynamic shared memory (the same for every launch of the
+// kernel) on the current device. The setting stays, so it is made once per device, noted in
+// `done`: each call costs the host about half a microsecond.
+constexpr int kMaxSettingDevices = 64;
+inline cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<bool> (&done)[kMaxSettingDevices]) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxSettingDevices) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (err == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return err;
 }
 
 // ------------------------------------------------------------------------------------

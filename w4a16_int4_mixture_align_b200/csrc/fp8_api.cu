@@ -24,7 +24,8 @@ bool misaligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p
 
 chord_status_t check_rows(int64_t rows) {
   if (rows < 0) return fail(CHORD_ERR_INVALID_ARG, "rows=%lld", (long long)rows);
-  if (rows >= (int64_t(1) << 31) - 256) return fail(CHORD_ERR_UNSUPPORTED, "rows=%lld >= 2^31 - 256", (long long)rows);
+  // the unit lists number up to two positions a row in 32 bits
+  if (rows >= int64_t(1) << 30) return fail(CHORD_ERR_UNSUPPORTED, "rows=%lld >= 2^30", (long long)rows);
   return CHORD_OK;
 }
 

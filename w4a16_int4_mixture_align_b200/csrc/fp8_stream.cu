@@ -323,7 +323,8 @@ cudaError_t launch(const Fp8Args& a, int split, cudaStream_t stream) {
   using Cfg = StreamCfg<TN>;
   static_assert(Cfg::kStages >= 3 && Cfg::kStages * Cfg::kStageBytes >= TN * kWRows * 4, "ring");
   auto kern = fp8_stream_kernel<TN>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  static std::atomic<bool> allowed[kMaxSettingDevices];
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), Cfg::kSmem, allowed);
   if (err != cudaSuccess) return err;
   StreamMaps maps;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;

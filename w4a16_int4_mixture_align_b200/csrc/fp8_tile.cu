@@ -397,7 +397,8 @@ template <int CG, int BN, int EPI>
 cudaError_t launch(const Fp8Args& a, cudaStream_t stream) {
   using Cfg = TileCfg<CG, BN>;
   auto kern = fp8_tile_kernel<CG, BN, EPI>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+  static std::atomic<bool> allowed[kMaxSettingDevices];
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];

@@ -448,31 +448,68 @@ __global__ void __launch_bounds__(32 * kFusedWarps) router_scored_align_kernel(
                                              reinterpret_cast<int*>(router_smem));
 }
 
-template <int PER, int C>
-cudaError_t launch_fused(const RouterArgs& p, int E, int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
-                         int32_t* expert_ids, int32_t* ntp, int32_t* offsets, cudaStream_t stream) {
-  auto kern = router_scored_align_kernel<PER, C>;
-  const size_t route = router_scratch_bytes(p.G) * kFusedWarps, sort = align_smem_bytes<kFusedWarps>(E);
-  const size_t smem = route > sort ? route : sort;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+// Larger batches sort by one cluster of kSortCtas CTAs of 32 warps, up to MAXS steps a warp;
+// still larger ones by the kernels of align.cu. 65536 slots of 48 experts take 9 us after the
+// router, against 21 of the three kernels.
+constexpr int kSortCtas = 8;
+template <int MAXS>
+constexpr int64_t kClusterSlots = int64_t(kSortCtas) * 32 * 32 * MAXS;
+
+template <int MAXS>
+__global__ void __launch_bounds__(1024) sort_cluster_kernel(const int32_t* ids, int64_t n, int E, int block_m,
+                                                            int64_t cap, int64_t nblocks, int32_t* sorted_ids,
+                                                            int32_t* expert_ids, int32_t* ntp, int32_t* offsets) {
+  extern __shared__ __align__(16) uint8_t router_smem[];
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int rank = int(cluster_rank());
+  align_body<kSortCtas, 32, MAXS>(ids, n, n * rank / kSortCtas, n * (rank + 1) / kSortCtas, rank, E, block_m, cap,
+                                  nblocks, sorted_ids, expert_ids, ntp, offsets, reinterpret_cast<int*>(router_smem));
+}
+
+// The most that 1024 experts need in any of these kernels is 152 KiB.
+constexpr int kMaxSmem = 160 * 1024;
+
+// Launches `kern` as clusters of `ctas` CTAs, one cluster in all, early.
+template <typename... Params, typename... Args>
+cudaError_t launch_one_cluster(void (*kern)(Params...), std::atomic<bool> (&allowed)[kMaxSettingDevices], int ctas,
+                               int threads, size_t smem, cudaStream_t stream, Args... args) {
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), kMaxSmem, allowed);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(C);
-  cfg.blockDim = dim3(32 * kFusedWarps);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, kern, p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets);
+  err = cudaLaunchKernelEx(&cfg, kern, args...);
   count_launches(1);
   return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <int PER, int C>
+cudaError_t launch_fused(const RouterArgs& p, int E, int block_m, int64_t cap, int64_t nblocks, int32_t* sorted_ids,
+                         int32_t* expert_ids, int32_t* ntp, int32_t* offsets, cudaStream_t stream) {
+  const size_t route = router_scratch_bytes(p.G) * kFusedWarps, sort = align_smem_bytes<kFusedWarps>(E);
+  static std::atomic<bool> allowed[kMaxSettingDevices];
+  return launch_one_cluster(router_scored_align_kernel<PER, C>, allowed, C, 32 * kFusedWarps, route > sort ? route : sort, stream,
+                            p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets);
+}
+
+template <int MAXS>
+cudaError_t launch_sort(const int32_t* ids, int64_t n, int E, int block_m, int64_t cap, int64_t nblocks,
+                        int32_t* sorted_ids, int32_t* expert_ids, int32_t* ntp, int32_t* offsets, cudaStream_t stream) {
+  static std::atomic<bool> allowed[kMaxSettingDevices];
+  return launch_one_cluster(sort_cluster_kernel<MAXS>, allowed, kSortCtas, 1024, align_smem_bytes<32>(E), stream, ids, n, E,
+                            block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets);
 }
 
 template <int PER>
@@ -484,8 +521,8 @@ cudaError_t launch_per(const RouterArgs& p, int E, int block_m, int64_t cap, int
   if (p.T <= kFusedMaxTokens)
     return launch_fused<PER, kFusedCtas>(p, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
   const size_t route = router_scratch_bytes(p.G) * kRouterWarps;
-  cudaError_t err = cudaFuncSetAttribute(router_scored_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(route));
+  static std::atomic<bool> allowed[kMaxSettingDevices];
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(router_scored_kernel<PER>), kMaxSmem, allowed);
   if (err != cudaSuccess) return err;
   const int64_t want = (p.T + kRouterWarps - 1) / kRouterWarps, most = int64_t(num_sms) * 8;
   err = launch_pdl(true, router_scored_kernel<PER>, dim3(unsigned(want < most ? want : most)), dim3(32 * kRouterWarps),
@@ -493,8 +530,12 @@ cudaError_t launch_per(const RouterArgs& p, int E, int block_m, int64_t cap, int
   count_launches(1);
   if (err == cudaSuccess) err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  return launch_align(p.topk_ids, p.T * p.k, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets,
-                      workspace, stream);
+  const int64_t n = p.T * p.k;
+  if (n <= kClusterSlots<8>)
+    return launch_sort<8>(p.topk_ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
+  if (n <= kClusterSlots<32>)
+    return launch_sort<32>(p.topk_ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, stream);
+  return launch_align(p.topk_ids, n, E, block_m, cap, nblocks, sorted_ids, expert_ids, ntp, offsets, workspace, stream);
 }
 
 }  // namespace
