@@ -96,14 +96,19 @@ struct Plan {
 // borders, in us, for 64-row streaming, 128 x 128, 128 x 256 and 256 x 256 tiles: 4096 x 7168
 // M=128 14.0, 19.7, 29.3, 29.8; M=384 35.7, 21.4, 30.1, 31.3; M=768 -, 37.6, 32.5, 32.5; M=4096
 // -, 175, 122, 121; 512 x 7168 M=512 11.5, 19.5, 29.1, 29.1; 7168 x 2048 M=384 23, 14.2, 13.2, 13.4.
-// `expected`: rows per expert; grouped experts are taken to hold up to 1.25 times as many, and
-// contiguous ones whole 128-row blocks.
+// 48 experts of 7168 x 2048 with two blocks each (contiguous): 209 us by 256 x 256 tiles, 222 by
+// 128 x 256, 277 by 128 x 128. `expected`: rows per expert; masked experts are taken to hold up
+// to 1.25 times as many.
 Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
   const int KB = fp8_blocks(a.K);
-  const double rows = a.layout == kFp8Masked ? 1.25 * expected : double(expected);
-  auto units_of = [&](int bm) {
-    const double per = a.layout == kFp8Contiguous && bm < 128 ? ceil(rows / 128) * (128 / bm) : ceil(rows / bm);
-    return int64_t(per * (a.layout == kFp8Dense ? 1 : a.E));
+  // contiguous: every 128-row block is a unit, or several; pairs of an expert's blocks are units
+  // of 256 rows where experts have more than one
+  const int64_t blocks = (a.rows + 127) / 128;
+  auto units_of = [&](int bm) -> int64_t {
+    if (a.layout == kFp8Dense) return (a.rows + bm - 1) / bm;
+    if (a.layout == kFp8Masked) return a.E * int64_t(ceil(1.25 * expected / bm));
+    if (bm <= 128) return blocks * (128 / bm);
+    return 2 * blocks >= 3 * int64_t(a.E) ? (blocks + 1) / 2 : blocks;
   };
   auto waves = [](int64_t items, int64_t slots) { return double((items + slots - 1) / slots); };
   Plan best{};
@@ -127,7 +132,7 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
   if (!(flags & CHORD_FLAG_FORCE_STREAM)) {
     offer(true, 128, 128, 1, 2.6 + waves(units_of(128) * ((a.N + 127) / 128), a.num_sms) * (KB * 0.31 + 1.2));
     offer(true, 256, 256, 1, 3.0 + waves(units_of(256) * ((a.N + 255) / 256), a.num_sms / 2) * (KB * 0.50 + 0.9));
-    offer(true, 128, 256, 1, 3.0 + waves(units_of(128) * ((a.N + 255) / 256), a.num_sms) * (KB * 0.50 + 0.9));
+    offer(true, 128, 256, 1, 3.0 + waves(units_of(128) * ((a.N + 255) / 256), a.num_sms) * (KB * 0.53 + 0.9));
   }
   return best;
 }
