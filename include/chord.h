@@ -383,9 +383,9 @@ CHORD_API chord_status_t chord_grouped_masked(const uint16_t* x, int E, int64_t 
  *   neither read nor written (counts are clamped to [0, max_m]).
  * chord_fp8_silu_quantize: the same of silu(h[r, 0:I]) * h[r, I:2I], computed in FP32; h:
  *   [rows, ldh] of h_dtype, ldh >= 2I. I % 16 == 0.
- * chord_fp8_gate_up: h = chord_fp8_gemm with w13 [2I, H] (gate rows first) kept in FP32,
- *   then chord_fp8_silu_quantize of it: q e4m3 [M, I] and scales [I/128, M], the operands
- *   of the down product. I % 128 == 0. workspace: >= chord_fp8_gate_up_workspace_bytes(M, I)
+ * chord_fp8_gate_up: the FP32 sums of chord_fp8_gemm with w13 [2I, H] (gate rows first)
+ *   through chord_fp8_silu_quantize: q e4m3 [M, I] and scales [I/128, M],
+ *   the operands of the down product. I % 128 == 0. workspace: >= chord_fp8_gate_up_workspace_bytes(M, I)
  *   bytes, rules as above.
  * ---------------------------------------------------------------------------------- */
 CHORD_API size_t chord_fp8_workspace_bytes(int64_t rows, int E);

@@ -315,7 +315,8 @@ def mlp_reference(xq, xs, w13, s13, w2, s2):
     return ref64.silu_mul(h)
 
 
-@pytest.mark.parametrize("M,H,I", [(1, 128, 128), (5, 400, 256), (16, 1024, 384), (130, 272, 128), (300, 512, 256)])
+@pytest.mark.parametrize("M,H,I", [(1, 128, 128), (5, 400, 256), (16, 1024, 384), (130, 272, 128), (300, 512, 256),
+                                   (1, 7168, 128), (33, 4096, 256), (70, 2048, 640), (2500, 272, 256)])
 @pytest.mark.parametrize("schedule", ["stream", "tensor", "auto"])
 def test_gate_up(chord, M, H, I, schedule):
     import torch

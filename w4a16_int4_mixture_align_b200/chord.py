@@ -43,6 +43,8 @@ CHORD_FLAG_FORCE_STREAM = 0x2
 CHORD_FLAG_FORCE_TENSOR = 0x4
 CHORD_FLAG_OUTPUT_FP32 = 0x8
 
+CHORD_WORKSPACE_HEADER_BYTES = 65536
+
 CHORD_DTYPE_F32 = 0
 CHORD_DTYPE_BF16 = 1
 CHORD_DTYPE_F16 = 2
@@ -636,7 +638,8 @@ class ChordFP8MLP:
         self.aq = _alloc_bytes(T * self.I, d)
         self.as_ = torch.empty(max(T * _blocks128(self.I), 1), dtype=torch.float32, device=d)
         need = max(chord_fp8_gate_up_workspace_bytes(T, self.I), chord_fp8_workspace_bytes(T, 1))
-        self.workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=d)
+        self.workspace = _alloc_bytes(need, d)
+        self.workspace[:CHORD_WORKSPACE_HEADER_BYTES].zero_()
         self.max_tokens = T
         self._pointers = (*self._weights, _ptr(self.xq), _ptr(self.xs), _ptr(self.aq), _ptr(self.as_),
                           _ptr(self.workspace), _nbytes(self.workspace))

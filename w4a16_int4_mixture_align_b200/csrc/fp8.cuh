@@ -90,6 +90,8 @@ cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t stream);
 // a.bm in {16, 32, 64}; `split` CTAs (a power of two up to 8, at most the k blocks) share an item.
 constexpr int kFp8StreamCtas = 2;  // resident per SM
 cudaError_t launch_fp8_stream(const Fp8Args& a, int split, cudaStream_t stream);
+// Dense gate_up as launch_fp8_tile_gate_up; clusters of 2 x split CTAs, split <= 4.
+cudaError_t launch_fp8_stream_gate_up(const Fp8Args& a, int split, cudaStream_t stream);
 // (a.bm, a.bn) of (128, 128), (128, 256): single CTAs; (256, 256): CTA pairs.
 cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream);
 // Dense, w = [gate; up] with a.N = 2 I: SiLU(gate) * up quantised to q [rows, I], scales [I/128, rows].

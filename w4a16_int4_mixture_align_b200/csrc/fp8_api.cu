@@ -81,6 +81,10 @@ int stream_split(int64_t items, int KB, int64_t slots) {
   return split;
 }
 
+// Estimates of the streaming kernel with units of 16, 32 and 64 rows, in us: to start, and per k
+// block of an item.
+constexpr double kStreamStart[3] = {4.6, 5.0, 6.4}, kStreamPerKb[3] = {0.37, 0.39, 0.52};
+
 struct Plan {
   bool tensor;  // the tile kernel (fp8_tile.cu) or the streaming one (fp8_stream.cu)
   int bm;       // rows of a unit
@@ -117,7 +121,6 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
     if (us < best.us) best = Plan{tensor, bm, bn, split, us};
   };
   if (!(flags & CHORD_FLAG_FORCE_TENSOR)) {
-    const double start[3] = {4.6, 5.0, 6.4}, per_kb[3] = {0.37, 0.39, 0.52};
     const int64_t slots = int64_t(a.num_sms) * kFp8StreamCtas, tiles = (a.N + 127) / 128;
     for (int i = 0; i < 3; ++i) {
       const int bm = 16 << i;
@@ -126,7 +129,7 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
       // a split grid covers every unit there may be, so it has to stay small
       const int64_t most = ((a.rows + bm - 1) / bm + (a.layout == kFp8Dense ? 0 : a.E)) * tiles;
       if (most * split > 8 * slots) split = 1;
-      offer(false, bm, 128, split, start[i] + waves(items * split, slots) * ((KB + split - 1) / split) * per_kb[i]);
+      offer(false, bm, 128, split, kStreamStart[i] + waves(items * split, slots) * ((KB + split - 1) / split) * kStreamPerKb[i]);
     }
   }
   if (!(flags & CHORD_FLAG_FORCE_STREAM)) {
@@ -165,16 +168,36 @@ chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices
   return err == cudaSuccess ? CHORD_OK : cuda_fail(err, tensor ? "FP8 tensor-core GEMM launch" : "FP8 streaming GEMM launch");
 }
 
-// Whether gate_up runs as one kernel (256-row x 128-column tiles), or as the product in FP32
-// and a quantisation: whichever is estimated to take less time. 4096 x 7168, in us, one kernel
-// and two: M=256 38.8, 28.9; M=512 39.9, 38.4; M=1024 41.0, 44.1; M=4096 149, 155.
-bool fused_gate_up(const Fp8Args& a, int flags) {
-  if (flags & CHORD_FLAG_FORCE_STREAM) return false;
-  if (flags & CHORD_FLAG_FORCE_TENSOR) return true;
-  const int64_t tiles = (a.rows + 255) / 256 * (a.N / 256), pairs = a.num_sms / 2;
-  const double fused = 3.0 + double((tiles + pairs - 1) / pairs) * (fp8_blocks(a.K) * 0.50 + 2.0);
-  const double quantise = 3.5 + double(a.rows) * a.N * 8 / 5e6;  // FP32 sums written and read
-  return fused < choose_plan(a, a.rows, flags).us + quantise;
+// The same for gate_up (a.N = 2 I): streaming by clusters of 2 x split CTAs or 256-row x 128-column
+// tiles, both ending in the quantised SiLU(gate) * up; or, for up to kTwoStepRows rows (split = 0),
+// the product in FP32 and a quantisation. In us for 4096 x 7168: M=16 9.8, 33.3, 12.1; M=128
+// 15.3, 33.6, 19.6; M=512 -, 34.9, 29.1; M=1024 -, 36.1, 41.4.
+constexpr int64_t kTwoStepRows = 1024;
+Plan choose_gate_up(const Fp8Args& a, int flags) {
+  const int KB = fp8_blocks(a.K);
+  Plan best{};
+  best.us = 1e30;
+  if (!(flags & CHORD_FLAG_FORCE_TENSOR)) {
+    const int64_t slots = int64_t(a.num_sms) * kFp8StreamCtas;
+    for (int i = 0; i < 3; ++i) {
+      const int bm = 16 << i;
+      const int64_t items = (a.rows + bm - 1) / bm * (a.N / 256);
+      const int most = stream_split(2 * items, KB, slots), split = most < 4 ? most : 4;
+      const double us = kStreamStart[i] + 1.0 +
+                        double((2 * items * split + slots - 1) / slots) * ((KB + split - 1) / split) * kStreamPerKb[i];
+      if (us < best.us) best = Plan{false, bm, 128, split, us};
+    }
+  }
+  if (!(flags & CHORD_FLAG_FORCE_STREAM)) {
+    const int64_t tiles = (a.rows + 255) / 256 * (a.N / 256), pairs = a.num_sms / 2;
+    const double us = 3.0 + double((tiles + pairs - 1) / pairs) * (KB * 0.50 + 2.0);
+    if (us < best.us) best = Plan{true, 256, 256, 1, us};
+  }
+  if (!(flags & (CHORD_FLAG_FORCE_TENSOR | CHORD_FLAG_FORCE_STREAM)) && a.rows <= kTwoStepRows) {
+    const double us = choose_plan(a, a.rows, flags).us + 4.5 + double(a.rows) * a.N * 8 / 5e6;
+    if (us < best.us) best = Plan{false, 0, 0, 0, us};
+  }
+  return best;
 }
 
 chord_status_t quantize(const void* x, int dtype, int64_t ld, int64_t rows, int K, int silu, const int32_t* masked_m,
@@ -293,7 +316,8 @@ chord_status_t chord_fp8_grouped_masked(const uint8_t* xq, const float* xs, int 
 
 size_t chord_fp8_gate_up_workspace_bytes(int64_t M, int I) {
   if (M < 0 || I < 1) return 0;
-  return chord_fp8_workspace_bytes(M, 1) + size_t(align256(uint64_t(M) * 2 * I * 4));
+  const int64_t sums = M < kTwoStepRows ? M : kTwoStepRows;  // FP32, rows of the two-step form
+  return chord_fp8_workspace_bytes(M, 1) + size_t(align256(uint64_t(sums) * 2 * I * 4));
 }
 
 chord_status_t chord_fp8_gate_up(const uint8_t* xq, const float* xs, int64_t M, int H, const uint8_t* w13,
@@ -312,17 +336,20 @@ chord_status_t chord_fp8_gate_up(const uint8_t* xq, const float* xs, int64_t M, 
   if ((st = current_device(&num_sms)) != CHORD_OK) return st;
   if (M == 0) return CHORD_OK;
   Fp8Args a = product_args(xq, xs, M, H, w13, ws13, 1, 2 * I, q, workspace, flags, kFp8Dense, num_sms);
-  if (fused_gate_up(a, flags)) {
-    a.out_scales = scales;
-    const cudaError_t err = launch_fp8_tile_gate_up(a, reinterpret_cast<cudaStream_t>(stream));
-    return err == cudaSuccess ? CHORD_OK : cuda_fail(err, "FP8 gate_up launch");
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const Plan plan = choose_gate_up(a, flags);
+  if (plan.split == 0) {
+    a.out = static_cast<uint8_t*>(workspace) + chord_fp8_workspace_bytes(M, 1);
+    a.out_f32 = 1;
+    st = run_product(a, M, nullptr, nullptr, 0, workspace, flags, cs);
+    if (st != CHORD_OK) return st;
+    return quantize(a.out, CHORD_DTYPE_F32, 2 * int64_t(I), M, I, 1, nullptr, 0, q, scales, cs);
   }
-  a.out = static_cast<uint8_t*>(workspace) + chord_fp8_workspace_bytes(M, 1);
-  a.out_f32 = 1;
-  st = run_product(a, M, nullptr, nullptr, 0, workspace, flags, reinterpret_cast<cudaStream_t>(stream));
-  if (st != CHORD_OK) return st;
-  return quantize(a.out, CHORD_DTYPE_F32, 2 * int64_t(I), M, I, 1, nullptr, 0, q, scales,
-                  reinterpret_cast<cudaStream_t>(stream));
+  a.out_scales = scales;
+  a.bm = plan.bm;
+  a.bn = plan.bn;
+  const cudaError_t err = plan.tensor ? launch_fp8_tile_gate_up(a, cs) : launch_fp8_stream_gate_up(a, plan.split, cs);
+  return err == cudaSuccess ? CHORD_OK : cuda_fail(err, "FP8 gate_up launch");
 }
 
 }  // extern "C"
