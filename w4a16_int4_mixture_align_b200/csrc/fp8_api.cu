@@ -98,8 +98,8 @@ struct Plan {
 // fitted to measurements on a B200 over M = 8 .. 4096 of 4096 x 7168, 7168 x 2048, 512 x 7168,
 // 576 x 1520 and 7168 x 256 (N x K); it lies within a quarter of them. On both sides of some
 // borders, in us, for 64-row streaming, 128 x 128, 128 x 256 and 256 x 256 tiles: 4096 x 7168
-// M=128 14.0, 19.7, 29.3, 29.8; M=384 35.7, 21.4, 30.1, 31.3; M=768 -, 37.6, 32.5, 32.5; M=4096
-// -, 175, 122, 121; 512 x 7168 M=512 11.5, 19.5, 29.1, 29.1; 7168 x 2048 M=384 23, 14.2, 13.2, 13.4.
+// M=128 14.0, 18.0, 29.3, 29.8; M=512 35.5, 19.9, 31.0, 31.3; M=1024 -, 36.0, 32.1, 32.6; M=4096
+// -, 170, 123, 122; 512 x 7168 M=512 11.5, 17.7, 29.1, 29.0; 7168 x 2048 M=512 25, 13.9, 13.3, 13.5.
 // 48 experts of 7168 x 2048 with two blocks each (contiguous): 209 us by 256 x 256 tiles, 222 by
 // 128 x 256, 277 by 128 x 128. `expected`: rows per expert; masked experts are taken to hold up
 // to 1.25 times as many.
@@ -133,7 +133,9 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
     }
   }
   if (!(flags & CHORD_FLAG_FORCE_STREAM)) {
-    offer(true, 128, 128, 1, 2.6 + waves(units_of(128) * ((a.N + 127) / 128), a.num_sms) * (KB * 0.31 + 1.2));
+    // (many waves of small tiles wait for L2)
+    const double small = waves(units_of(128) * ((a.N + 127) / 128), a.num_sms);
+    offer(true, 128, 128, 1, 2.6 + small * (KB * (small > 3 ? 0.32 : 0.265) + 1.4));
     offer(true, 256, 256, 1, 3.0 + waves(units_of(256) * ((a.N + 255) / 256), a.num_sms / 2) * (KB * 0.50 + 0.9));
     offer(true, 128, 256, 1, 3.0 + waves(units_of(128) * ((a.N + 255) / 256), a.num_sms) * (KB * 0.53 + 0.9));
   }

@@ -5,7 +5,8 @@
 //
 // The FP32 scales are arbitrary, so the tensor core cannot apply them: it forms P_kb, the
 // product of one 128-wide k block, in tensor memory, and CUDA cores add s * P_kb to FP32
-// registers while it forms the next one in the other of two buffers. Activation rows are
+// registers while it forms the next one in another of two buffers (four
+// of 128 columns). Activation rows are
 // the M side, so a thread owns one row and a block costs it one scale and one fused
 // multiply-add per column.
 //
@@ -22,12 +23,13 @@
 // half of the weight rows, so a CTA fetches 32 KiB per 256 x 256 x 128 step instead of the 48
 // of a single 128 x 256 tile. At 8192 x 4096 x 7168 (M x N x K) the pairs take 220 us and the
 // single tiles 228, at 4096 rows 121 and 122; the single ones serve units of 128 rows. 128 x
-// 128 tiles serve products of few tiles (512 rows: 21 us against 31).
+// 128 tiles serve products of few tiles (512 rows: 20 us against 31).
 //
 // Bound: the round trip of a tensor-memory buffer. Measured in cycles, a block's MMAs take
 // 660 (an instruction of K = 32 takes 130 to 165 whatever its N), their end is seen 340
 // later, reading the buffer takes 440 and handing it back 500; with two buffers that is about
-// 1000 a block, 2.2 PFLOP/s. The TMA feed alone would allow 660 (3.2 PFLOP/s while operands
+// 1000 a block, 2.2 PFLOP/s. Tiles of 128 columns have four buffers and run at their MMAs'
+// pace, 520 for half the work. The TMA feed alone would allow 660 (3.2 PFLOP/s while operands
 // stay in L2), the FP32 additions 256.
 //
 // All waits are bounded. On a timeout a CTA raises CHORD_DEV_TIMEOUT, waits (bounded) for
@@ -57,6 +59,7 @@ struct TileCfg {
   static constexpr int kStages = kSmemBudget / kStageBytes > 8 ? 8 : kSmemBudget / kStageBytes;
   static constexpr int kSmemBytes = 1024 + kFixedBytes + kStages * kStageBytes + kOutBytes;
   static constexpr int kCols = BN / 2;         // columns of a promotion warp
+  static constexpr int kBufs = 512 / BN;       // tensor-memory buffers
 };
 
 // Registers per thread: 384 threads launch with 168 each (64512 together); the 256 promotion
@@ -127,7 +130,7 @@ template <int CG, int BN, int EPI>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fp8_tile_kernel(const __grid_constant__ TileMaps maps, const Fp8Args p) {
   using Cfg = TileCfg<CG, BN>;
-  constexpr int S = Cfg::kStages, COLS = Cfg::kCols;
+  constexpr int S = Cfg::kStages, COLS = Cfg::kCols, B = Cfg::kBufs;
   static_assert(EPI == kRows || (CG == 2 && BN == 256), "the gate_up tile");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -136,8 +139,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* done = full + S;                           // [S] stage multiplied: it may be refilled, its
                                                        // product read (one commit a block: each holds a
                                                        // pair's MMAs up by about 400 cycles)
-  uint64_t* acc_empty = done + S;                      // [2] buffer read by every warp (rank 0's is used)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* acc_empty = done + S;                      // [B] buffer read by every warp (rank 0's is used)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + B);
   __shared__ int abort_flag;
   // kGateUp: maxima of the rows by column half, in the half of a staging box it does not use
   uint32_t(*row_max)[kBM] =
@@ -151,14 +154,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&done[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < B; ++b) {
       mbar_init(&acc_empty[b], kPromoteWarps * CG);
     }
     fence_barrier_init();
   }
   __syncthreads();
   if (CG == 2) cluster_sync_all();  // the peer's barriers exist before anything arrives on them
-  if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
+  if (warp == 1) tmem_alloc<CG>(tmem_slot, B * BN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -214,13 +217,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // its thread for about their time, so a single issuer's waits and commits between two
       // blocks were time that the tensor core stood still
       constexpr uint32_t idesc = idesc_e4m3(kBM * CG, BN);
-      const uint32_t b = warp == 1 ? 0 : 1;  // its tensor-memory buffer
       const uint32_t blocks = uint32_t(cid < tiles ? (tiles - cid + ncl - 1) / ncl : 0) * uint32_t(KB);
-      uint32_t it = b;
+      uint32_t it = warp == 1 ? 0 : 1;
       for (; it < blocks; it += 2) {
-        const uint32_t s = it % S;
+        const uint32_t s = it % S, b = it % B;
         if (!mbar_wait(&full[s], (it / S) & 1, abort_v, p.status) ||
-            (it >= 2 && !mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1, abort_v, p.status)))
+            (it >= B && !mbar_wait(&acc_empty[b], ((it / B) - 1) & 1, abort_v, p.status)))
           break;
         tc_fence_after();
         const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes;
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint32_t v[2][W];
       ok = mbar_wait_warp(&done[it % S], (it / S) & 1, abort_v, p.status);
       tc_fence_after();
-      tmem_ld_async(src + (it & 1) * BN, v[0]);
+      tmem_ld_async(src + (it % B) * BN, v[0]);
 #pragma unroll 1
       for (int kb = 0; kb < KB; ++kb) {
         const uint64_t s = pack2(x0 * w0, x0 * w0), s_up = EPI == kGateUp ? pack2(x0 * u0, x0 * u0) : s;
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           w1 = __ldg(ws + kb + 2);
           if (EPI == kGateUp) u1 = __ldg(wu + kb + 2);
         }
-        const uint32_t b = it & 1;
+        const uint32_t b = it % B;
         ++it;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (kb + 1 < KB) ok = ok && mbar_wait_warp(&done[it % S], (it / S) & 1, abort_v, p.status);
             tc_fence_after();
             // after the last block this rereads a buffer of this CTA, for nothing
-            tmem_ld_async(src + (it & 1) * BN, v[0]);
+            tmem_ld_async(src + (it % B) * BN, v[0]);
           }
 #pragma unroll
           for (int j = 0; j < W; j += 2)
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (CG == 2) cluster_sync_all();  // nothing of either CTA is in flight towards the other
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<CG>(tmem, 2 * BN);
+    tmem_dealloc<CG>(tmem, B * BN);
   }
 }
 
