@@ -64,14 +64,16 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
-// The scale of a block and its inverse from the bits of its largest |x| (as integers a NaN is
+// The scale of a block (or its inverse) from the bits of its largest |x| (as integers a NaN is
 // above infinity, infinity above the rest; both give a NaN scale).
-__device__ __forceinline__ void block_scale(uint32_t amax_bits, float* scale, float* inverse) {
+__device__ __forceinline__ float block_quotient(uint32_t amax_bits, bool inverse) {
   const float amax = fmaxf(__uint_as_float(amax_bits), 0x1p-100f);
-  const float nan = __uint_as_float(0x7fffffffu);
-  const bool finite = amax_bits < 0x7f800000u;
-  *scale = finite ? __fdiv_rn(amax, kFp8Max) : nan;
-  *inverse = finite ? __fdiv_rn(kFp8Max, amax) : nan;
+  const float q = __fdiv_rn(inverse ? kFp8Max : amax, inverse ? amax : kFp8Max);
+  return amax_bits < 0x7f800000u ? q : __uint_as_float(0x7fffffffu);
+}
+__device__ __forceinline__ void block_scale(uint32_t amax_bits, float* scale, float* inverse) {
+  *scale = block_quotient(amax_bits, false);
+  *inverse = block_quotient(amax_bits, true);
 }
 // silu(g) * u. The reciprocal of d = 1 + exp(-g) is the hardware's approximation and one step
 // of Newton's iteration, half the instructions of a division; below -80, where exp(-g) nears
