@@ -32,7 +32,7 @@ struct Raw {
 };
 __device__ __forceinline__ uint4 ldg_once(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, DTYPE == CHORD_DTYPE_BF16 &&
   if (row >= a.rows) return;
   if (a.masked_m) {
     const int64_t e = row / a.max_m;
-    if (row - e * a.max_m >= __ldg(a.masked_m + e)) return;
+    if (row - e * a.max_m >= __ldcg(a.masked_m + e)) return;
   }
   Raw<DTYPE> raw[kSteps], raw_up[SILU ? kSteps : 1];
   (void)raw_up;

@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
   const int items = units * NT;
   const int first = ctas > 1 ? int(cluster_id_x()) : int(blockIdx.x);
   const int step = ctas > 1 ? int(num_clusters_x()) : int(gridDim.x);  // a grid of clusters covers all items
-  auto unit_row0 = [&](int u) { return p.layout == kFp8Dense ? u * TN : __ldg(p.block_row0 + u); };
-  auto unit_expert = [&](int u) { return p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u); };
+  auto unit_row0 = [&](int u) { return p.layout == kFp8Dense ? u * TN : __ldcg(p.block_row0 + u); };
+  auto unit_expert = [&](int u) { return p.layout == kFp8Dense ? 0 : __ldcg(p.expert_ids + u); };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
           const int at = 32 * j + lane, kb = kb0 + at / TN;
           const int64_t row = row0 + at % TN;
           // rows and blocks that do not exist are never used
-          v[j] = kb < kb_end && row < p.rows ? __ldg(p.xs + kb * p.rows + row) * __ldg(ws + kb) : 0.f;
+          v[j] = kb < kb_end && row < p.rows ? __ldcg(p.xs + kb * p.rows + row) * __ldcg(ws + kb) : 0.f;
         }
         if (grp >= Cfg::kGroups && !mbar_wait_warp(&sc_empty[g], ((grp / Cfg::kGroups) - 1) & 1, abort_v, p.status)) {
           ok = false;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
 #pragma unroll
       for (int j0 = 0; j0 < TN; j0 += 32) {
         const int j = j0 + lane;
-        const bool mine = j < TN && (p.layout == kFp8Dense ? row0 + j < p.rows : __ldg(p.sorted_ids + u * TN + j) >= 0);
+        const bool mine = j < TN && (p.layout == kFp8Dense ? row0 + j < p.rows : __ldcg(p.sorted_ids + u * TN + j) >= 0);
         const uint32_t live = __ballot_sync(0xffffffffu, mine);
         if (n >= p.N) continue;
 #pragma unroll
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
       // four neighbouring columns a thread, every CTA's share requested before any is added
       for (int i = threadIdx.x; i < (j_end - j_begin) * (kWRows / 4); i += kThreads) {
         const int j = j_begin + i / (kWRows / 4), c0 = i % (kWRows / 4) * 4, n = n0 + c0;
-        const bool live = p.layout == kFp8Dense ? row0 + j < p.rows : __ldg(p.sorted_ids + u * TN + j) >= 0;
+        const bool live = p.layout == kFp8Dense ? row0 + j < p.rows : __ldcg(p.sorted_ids + u * TN + j) >= 0;
         if (!live || n >= p.N) continue;  // N % 8 == 0: four columns are all in or all out
         const float* mine = partial + j * kWRows + c0;
         float4 part[kMaxSplit];

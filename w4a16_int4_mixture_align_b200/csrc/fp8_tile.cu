@@ -191,9 +191,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int t = cid; t < tiles && ok; t += ncl) {
           const int u = t / NT, nt = t - u * NT;
           int row;
-          if (of_x) row = (p.layout == kFp8Dense ? u * kBM * CG : __ldg(p.block_row0 + u)) + int(rank) * kBM;
+          if (of_x) row = (p.layout == kFp8Dense ? u * kBM * CG : __ldcg(p.block_row0 + u)) + int(rank) * kBM;
           else if (EPI == kGateUp) row = int(rank) * I + nt * kFp8Block;
-          else row = (p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u)) * p.N + nt * BN + int(rank) * Cfg::kBRows;
+          else row = (p.layout == kFp8Dense ? 0 : __ldcg(p.expert_ids + u)) * p.N + nt * BN + int(rank) * Cfg::kBRows;
           for (int kb = 0; kb < KB; ++kb, ++fill) {
             const uint32_t s = fill % S;
             if (fill >= S && !mbar_wait(&done[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
@@ -253,10 +253,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int t = cid; t < tiles && (ok || EPI == kGateUp); t += ncl) {
       const int u = t / NT;
       const int n0 = EPI == kGateUp ? (t - u * NT) * kFp8Block + h * 64 : (t - u * NT) * BN + h * COLS;
-      const int e = p.layout == kFp8Dense ? 0 : __ldg(p.expert_ids + u);
+      const int e = p.layout == kFp8Dense ? 0 : __ldcg(p.expert_ids + u);
       const int pos = u * kBM * CG + int(rank) * kBM + r;
-      const int64_t row = p.layout == kFp8Dense ? pos : __ldg(p.block_row0 + u) + int(rank) * kBM + r;
-      const bool live = p.layout == kFp8Dense ? row < p.rows : __ldg(p.sorted_ids + pos) >= 0;
+      const int64_t row = p.layout == kFp8Dense ? pos : __ldcg(p.block_row0 + u) + int(rank) * kBM + r;
+      const bool live = p.layout == kFp8Dense ? row < p.rows : __ldcg(p.sorted_ids + pos) >= 0;
       // scales: one per row (rows that are not stored read row 0's), one for the columns
       const float* xs = p.xs + (row < p.rows ? row : 0);
       const int nb = min(n0 / kFp8Block, NB - 1);
@@ -266,13 +266,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int c = 0; c < COLS / 2; ++c) sum[c] = 0;
       // the scales of this k block and the next two (loads run two blocks ahead)
-      float x0 = __ldg(xs), w0 = __ldg(ws), x1 = 0.f, w1 = 0.f;
-      float u0 = EPI == kGateUp ? __ldg(wu) : 0.f, u1 = 0.f;
+      float x0 = __ldcg(xs), w0 = __ldcg(ws), x1 = 0.f, w1 = 0.f;
+      float u0 = EPI == kGateUp ? __ldcg(wu) : 0.f, u1 = 0.f;
       if (KB > 1) {
         xs += p.rows;
-        x1 = __ldg(xs);
-        w1 = __ldg(ws + 1);
-        if (EPI == kGateUp) u1 = __ldg(wu + 1);
+        x1 = __ldcg(xs);
+        w1 = __ldcg(ws + 1);
+        if (EPI == kGateUp) u1 = __ldcg(wu + 1);
       }
       // the tensor-memory loads run one chunk of columns ahead of the additions, across k
       // blocks too
@@ -289,9 +289,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         u0 = u1;
         if (kb + 2 < KB) {
           xs += p.rows;
-          x1 = __ldg(xs);
-          w1 = __ldg(ws + kb + 2);
-          if (EPI == kGateUp) u1 = __ldg(wu + kb + 2);
+          x1 = __ldcg(xs);
+          w1 = __ldcg(ws + kb + 2);
+          if (EPI == kGateUp) u1 = __ldcg(wu + kb + 2);
         }
         const uint32_t b = it % B;
         ++it;

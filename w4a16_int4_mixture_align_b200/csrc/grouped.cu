@@ -72,11 +72,11 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* s_warp, int* tot
 // four m_indices entries from row `row` (16-byte aligned when row + 3 < M); rows past M
 // read as padding
 __device__ __forceinline__ int4 load_ids4(const int32_t* __restrict__ m, int64_t row, int64_t M) {
-  if (row + 3 < M) return __ldg(reinterpret_cast<const int4*>(m + row));
+  if (row + 3 < M) return __ldcg(reinterpret_cast<const int4*>(m + row));
   int4 v = make_int4(-1, -1, -1, -1);
-  if (row < M) v.x = __ldg(m + row);
-  if (row + 1 < M) v.y = __ldg(m + row + 1);
-  if (row + 2 < M) v.z = __ldg(m + row + 2);
+  if (row < M) v.x = __ldcg(m + row);
+  if (row + 1 < M) v.y = __ldcg(m + row + 1);
+  if (row + 2 < M) v.z = __ldcg(m + row + 2);
   return v;
 }
 
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kRouteThreads) grouped_route_masked_kernel(
   bool bad = false;
   int cnt = 0, units = 0;
   if (tid < E) {
-    int64_t v = __ldg(masked_m + tid);
+    int64_t v = __ldcg(masked_m + tid);
     if (v < 0 || v > max_m) {
       bad = true;
       v = v < 0 ? 0 : max_m;

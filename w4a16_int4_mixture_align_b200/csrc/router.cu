@@ -57,8 +57,8 @@ constexpr float kLowestF32 = -3.402823466e38f, kLowestBf16 = -3.38953139e38f, kL
 // The logit, -inf where it masks its expert, +inf as the largest finite value.
 __device__ __forceinline__ float masked_logit(float v, float lowest) { return v > lowest ? fminf(v, -lowest) : -INFINITY; }
 __device__ __forceinline__ float load_logit(const RouterArgs& p, int64_t row, int e) {
-  if (p.dtype == CHORD_DTYPE_F32) return masked_logit(__ldg(static_cast<const float*>(p.logits) + row + e), kLowestF32);
-  const uint16_t bits = __ldg(static_cast<const uint16_t*>(p.logits) + row + e);
+  if (p.dtype == CHORD_DTYPE_F32) return masked_logit(__ldcg(static_cast<const float*>(p.logits) + row + e), kLowestF32);
+  const uint16_t bits = __ldcg(static_cast<const uint16_t*>(p.logits) + row + e);
   if (p.dtype == CHORD_DTYPE_BF16) return masked_logit(__uint_as_float(uint32_t(bits) << 16), kLowestBf16);
   return masked_logit(__half2float(__ushort_as_half(bits)), kLowestF16);
 }
@@ -208,7 +208,7 @@ __device__ __noinline__ void route_exact(const RouterArgs& p, int64_t t, float l
   for (int e = lane; e < p.G; e += 32) {
     const float l = load_logit(p, t * p.ld, e);
     double c = -INFINITY;
-    if (l > -INFINITY) c = p.bias ? score64(p, l, lmax, rz) + double(__ldg(p.bias + e)) : double(l);
+    if (l > -INFINITY) c = p.bias ? score64(p, l, lmax, rz) + double(p.bias[e]) : double(l);
     c64[e] = c;
   }
   __syncwarp();
@@ -281,14 +281,14 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
   if (p.dtype == CHORD_DTYPE_F32) {
     const float* row = static_cast<const float*>(p.logits) + t * p.ld;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = lane + 32 * i < p.G ? masked_logit(__ldg(row + lane + 32 * i), kLowestF32) : -INFINITY;
+    for (int i = 0; i < PER; ++i) l[i] = lane + 32 * i < p.G ? masked_logit(__ldcg(row + lane + 32 * i), kLowestF32) : -INFINITY;
   } else {
     const uint16_t* row = static_cast<const uint16_t*>(p.logits) + t * p.ld;
     const bool half = p.dtype == CHORD_DTYPE_F16;
     const float lowest = half ? kLowestF16 : kLowestBf16;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const uint32_t bits = lane + 32 * i < p.G ? __ldg(row + lane + 32 * i) : 0u;
+      const uint32_t bits = lane + 32 * i < p.G ? __ldcg(row + lane + 32 * i) : 0u;
       const float v = half ? __half2float(__ushort_as_half(uint16_t(bits))) : __uint_as_float(bits << 16);
       l[i] = lane + 32 * i < p.G ? masked_logit(v, lowest) : -INFINITY;
     }
@@ -296,7 +296,7 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
   float b[PER];
   if (p.bias) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) b[i] = lane + 32 * i < p.G ? __ldg(p.bias + lane + 32 * i) : 0.f;
+    for (int i = 0; i < PER; ++i) b[i] = lane + 32 * i < p.G ? p.bias[lane + 32 * i] : 0.f;
   }
   float lmax = 0.f, rz32 = 1.f;
   if (p.score == CHORD_SCORE_SOFTMAX) {
@@ -384,13 +384,13 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
   __syncwarp();
   double s = 0.0, rz = double(rz32);
   if (mine) s = score64(p, lc, lmax, rz);
-  double key = mine ? (p.bias ? s + double(__ldg(p.bias + e)) : double(lc)) : -INFINITY;
+  double key = mine ? (p.bias ? s + double(p.bias[e]) : double(lc)) : -INFINITY;
   int rank = rank_of(key, n, keys);
   if (p.bias && p.score == CHORD_SCORE_SOFTMAX && any_closer(key, n, 2.0 * kSlackAbs)) {
     // the denominator's FP32 error could swap two experts: once more with it in FP64
     rz = softmax_sum64(p, t, lmax);
     if (mine) s = score64(p, lc, lmax, rz);
-    if (mine) key = s + double(__ldg(p.bias + e));
+    if (mine) key = s + double(p.bias[e]);
     rank = rank_of(key, n, keys);
   }
   const bool chosen = mine && rank < p.k;
