@@ -22,8 +22,10 @@
 // than the error bound, more than 32 candidates, or k > 32 take the slow way: every c in
 // FP64 in shared memory, then k rounds of a warp-wide maximum.
 //
-// Bound: reading the logits (T=8192, G=384, FP32: 12.6 MB) and, below that, issue slots:
-// about 30 instructions per expert slot of a lane.
+// Bound: 8192 tokens of 384 FP32 logits take 15 us where reading them (12.6 MB) would take 2: a
+// token is about 1100 instructions, many of them dependent, and 32 warps fit an SM, so the
+// batch is two rounds of 5 us. One token is 4 us of that chain and 3 more of instruction
+// fetches; the sort behind it adds 3.
 #include <math.h>
 
 #include "align_common.cuh"
