@@ -479,3 +479,109 @@ def test_far_rows(chord):
         chord.chord_fp8_gemm(xq, xs, cuda(wq), cuda(ws), out, workspace(chord, rows), flag(chord, schedule))
         check_rows(out, y, a, K, slice(rows - 16, rows))
         assert (out[:-16] == 0).all()
+
+
+# More items than the kernels have CTAs, so that each takes several in turn: rings, buffers and
+# output staging carry over from one item to the next.
+@pytest.mark.parametrize("M,N,K,schedule", [(200, 13000, 400, "stream"), (16, 40008, 272, "stream"),
+                                            (1100, 4104, 272, "tensor"), (6000, 4104, 400, "tensor"),
+                                            (3001, 40008, 144, "tensor"), (6000, 4104, 400, "auto")])
+def test_several_items_a_cta(chord, M, N, K, schedule):
+    import torch
+    xq, wq = codes((M, K), M), codes((N, K), N)
+    xs, ws = scales((-(-K // B), M), 3), scales((-(-N // B), -(-K // B)), 4)
+    args, work = [cuda(v) for v in (xq, xs, wq, ws)], workspace(chord, M)
+    rows = np.unique(np.r_[0, M - 1, np.random.default_rng(M).integers(0, M, 60)])
+    y, a = ref64.product(xq[rows], xs[:, rows], wq, ws)
+    for dtype in (torch.bfloat16, torch.float32):
+        out = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
+        chord.chord_fp8_gemm(*args, out, work, flag(chord, schedule))
+        assert torch.isfinite(out).all()
+        check_rows(out[torch.from_numpy(rows).cuda()], y, a, K)
+    assert chord.chord_moe_check_status(work) == 0
+
+
+@pytest.mark.parametrize("layout", ["masked", "contiguous"])
+@pytest.mark.parametrize("schedule", ["stream", "tensor", "auto"])
+def test_many_experts(chord, layout, schedule):
+    """Experts with no row, one, a few tiles and parts of them; several units a CTA."""
+    import torch
+    E, N, K, max_m = 40, 1032, 272, 384
+    rng = np.random.default_rng(11)
+    counts = rng.choice([0, 1, 77, 128, 129, 300, 384], E)
+    if layout == "masked":
+        m = np.where(np.arange(max_m)[None, :] < counts[:, None], np.arange(E)[:, None], -1).ravel()
+    else:  # experts out of order, each padded to whole 128-row blocks
+        m = np.concatenate([np.r_[np.full(counts[e], e), np.full(-counts[e] % 128, -1)] for e in rng.permutation(E)])
+    m = m.astype(np.int32)
+    rows = m.size
+    xq, wq = codes((rows, K), rows), codes((E * N, K), 2).reshape(E, N, K)
+    xs, ws = scales((-(-K // B), rows), 3), scales((E, -(-N // B), -(-K // B)), 4)
+    xq[m < 0], xs[:, m < 0] = 0x7F, np.nan
+    work = workspace(chord, rows, E)
+    out = torch.full((rows, N), -7.0, dtype=torch.bfloat16, device="cuda")
+    x = [cuda(xq), cuda(xs)]
+    tail = [cuda(wq), cuda(ws), out, work, flag(chord, schedule)]
+    if layout == "masked":
+        chord.chord_fp8_grouped_masked(*x, cuda(counts.astype(np.int32)), 200, *tail)
+    else:
+        chord.chord_fp8_grouped_contiguous(*x, cuda(m), *tail)
+    assert (out[torch.from_numpy(m < 0).cuda()] == -7).all()
+    assert torch.isfinite(out).all() and chord.chord_moe_check_status(work) == 0
+    for e in range(E):
+        at = np.flatnonzero(m == e)
+        if at.size:
+            at = np.unique(np.r_[at[0], at[-1], rng.choice(at, 6)])
+            check_rows(out, *ref64.product(xq[at], xs[:, at], wq[e], ws[e]), K, at)
+
+
+@pytest.mark.parametrize("M,H,I,schedule", [(500, 400, 2560, "stream"), (6000, 272, 1280, "tensor")])
+def test_gate_up_several_items_a_cta(chord, M, H, I, schedule):
+    import torch
+    xq, w13 = codes((M, H), M), codes((2 * I, H), 5)
+    xs, s13 = scales((-(-H // B), M), 3), scales((2 * I // B, -(-H // B)), 4) * np.float32(2.0 ** -6)
+    args = [cuda(v) for v in (xq, xs, w13, s13)]
+    q = torch.zeros((M, I), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((I // B, M), device="cuda")
+    work = torch.zeros(chord.chord_fp8_gate_up_workspace_bytes(M, I), dtype=torch.uint8, device="cuda")
+    chord.chord_fp8_gate_up(*args, q, s, work, flag(chord, schedule))
+    assert chord.chord_moe_check_status(work) == 0
+    rows = np.unique(np.r_[0, M - 1, np.random.default_rng(M).integers(0, M, 60)])
+    h, ha = ref64.product(xq[rows], xs[:, rows], w13, s13)
+    off = ref64.product_bound(h, ha, H, False)
+    a, g, u = ref64.silu_mul(h), h[:, :I], h[:, I:]
+    aoff = 1.1 * off[:, :I] * np.abs(u) + np.abs(g) * off[:, I:] + 1.1 * off[:, :I] * off[:, I:] + np.abs(a) * 8 * 2.0 ** -24
+    amax, amax_off = (v.reshape(rows.size, -1, B).max(2) for v in (np.abs(a), aoff))
+    got_s = s.cpu().numpy().T.astype(np.float64)[rows]
+    assert (np.abs(got_s - amax / 448) <= (amax_off + amax * 2.0 ** -23) / 448).all()
+    v = ref64.CODES[q.cpu().numpy()[rows]] * np.repeat(got_s, B, 1)
+    step = np.maximum(np.abs(a) * 2.0 ** -4, np.repeat(got_s, B, 1) * 2.0 ** -10)
+    assert (np.abs(v - a) <= step * (1 + 2.0 ** -3) + aoff * (1 + 2.0 ** -3) + 1e-37).all()
+    # every row was written: no block of real sums is all zero
+    assert (s > 0).all() and (q != 0).any(1).all()
+
+
+def test_mlps_in_a_row(chord):
+    """Two layers that feed each other, twenty times without a wait between them, give the bits of
+    calls made one at a time."""
+    import torch
+    H, I, T = 512, 256, 40
+    a, b = (chord.ChordFP8MLP(*[cuda(v) for v in (codes((2 * I, H), k), scales((4, 4), k) * np.float32(0.004),
+                                                  codes((H, I), k + 1), scales((4, 2), k) * np.float32(0.004))], max_tokens=T)
+            for k in (5, 9))
+    x0 = torch.randn((T, H), device="cuda").to(torch.bfloat16)
+
+    def run(wait):
+        x = x0
+        for _ in range(10):
+            for layer in (a, b):
+                y = layer(x)
+                # back to rows of size 1, so that the values stay in range
+                x = (y.float() / y.float().abs().amax(1, keepdim=True).clamp_min(1e-30)).to(torch.bfloat16)
+                if wait:
+                    torch.cuda.synchronize()
+        return x
+    want = run(True)
+    assert torch.isfinite(want).all()
+    for _ in range(3):
+        assert torch.equal(run(False), want)

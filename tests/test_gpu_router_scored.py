@@ -187,3 +187,28 @@ def test_graph_replay_and_other_stream(chord):
     torch.cuda.synchronize()
     ref, _ = ref64.route(x.double().cpu().numpy(), LOWEST["float32"], None, 8, "sigmoid", 1, 1, 1, True, 1.0)
     np.testing.assert_array_equal(ids.cpu().numpy(), ref)
+
+
+# The sort behind the router: one CTA up to 16 tokens, one cluster up to 256, a cluster kernel up to
+# 65536 and up to 262144 slots, then the kernels of the plain sort; both sides of each border.
+@pytest.mark.parametrize("T,G,k,E,bm", [(16, 128, 64, 128, 8), (17, 128, 64, 128, 8), (256, 128, 64, 100, 16),
+                                        (257, 128, 64, 100, 16), (8192, 64, 8, 64, 128), (8193, 64, 8, 64, 128),
+                                        (8193, 1024, 8, 1024, 4), (32768, 64, 8, 9, 64), (32769, 64, 8, 9, 64)])
+def test_sorts(chord, T, G, k, E, bm):
+    b = (0.1 * np.random.default_rng(G).standard_normal(G)).astype(np.float32)
+    check(chord, normal(T, G, T), b, k, E, bm)
+
+
+def test_every_token_masked(chord):
+    """A batch of padding alone routes nothing."""
+    import torch
+    for T in (3, 200, 3000):
+        got = check(chord, torch.full((T, 96), float("-inf"), device="cuda"), np.ones(96, np.float32), 4, 96, 16)
+        assert (got[0] == -1).all() and int(got[4][0]) == 0
+
+
+def test_all_tokens_to_the_same_experts(chord):
+    """The longest run of one expert, with ties everywhere."""
+    import torch
+    for T in (16, 256, 5000):
+        check(chord, torch.zeros((T, 256), device="cuda"), None, 8, 4, 64)
