@@ -9,7 +9,6 @@
 namespace chord {
 namespace {
 
-
 __device__ __forceinline__ int ld_cluster_i32(uint32_t addr) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");

@@ -362,8 +362,9 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 // that kernel writes, and grid_dep_wait() returns once that kernel has completed and its
 // memory is visible. What it wrote is then read by ordinary loads or past L1 (__ldcg), not as
 // read-only data (__ldg): that would have to stay unchanged while this kernel runs, and it
-// was still being written when this kernel started. grid_dep_trigger() lets this kernel's own dependent launch before
-// this kernel finishes. Both are no-ops for a kernel launched without the attribute.
+// was still being written when this kernel started. grid_dep_trigger() lets this kernel's own
+// dependent launch before this kernel finishes. Both are no-ops for a kernel launched without
+// the attribute.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

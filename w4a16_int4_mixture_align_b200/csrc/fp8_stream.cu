@@ -104,9 +104,7 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
       mbar_init(&full[s], 1);
       mbar_init(&done[s], 1);
     }
-    for (int b = 0; b < B; ++b) {
-      mbar_init(&acc_empty[b], kPromote);
-    }
+    for (int b = 0; b < B; ++b) mbar_init(&acc_empty[b], kPromote);
     for (int g = 0; g < Cfg::kGroups; ++g) {
       mbar_init(&sc_full[g], 32);
       mbar_init(&sc_empty[g], kPromote);
@@ -361,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
 template <int TN, int OUT>
 cudaError_t launch(const Fp8Args& a, int split, cudaStream_t stream) {
   using Cfg = StreamCfg<TN>;
-  static_assert(Cfg::kStages >= 3 && Cfg::kStages * Cfg::kStageBytes >= TN * kWRows * 4, "ring");
+  static_assert(Cfg::kStages >= Cfg::kBufs, "a stage's barrier must not complete twice before its product is read");
+  static_assert(Cfg::kStages * Cfg::kStageBytes >= TN * kWRows * 4, "the sums fit where the ring was");
   auto kern = fp8_stream_kernel<TN, OUT>;
   static std::atomic<bool> allowed[kMaxSettingDevices];
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), Cfg::kSmem, allowed);

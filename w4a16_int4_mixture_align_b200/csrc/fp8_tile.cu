@@ -5,10 +5,9 @@
 //
 // The FP32 scales are arbitrary, so the tensor core cannot apply them: it forms P_kb, the
 // product of one 128-wide k block, in tensor memory, and CUDA cores add s * P_kb to FP32
-// registers while it forms the next one in another of two buffers (four
-// of 128 columns). Activation rows are
-// the M side, so a thread owns one row and a block costs it one scale and one fused
-// multiply-add per column.
+// registers while it forms the next one in another of two buffers (four of 128 columns).
+// Activation rows are the M side, so a thread owns one row and a block costs it one scale and
+// one fused multiply-add per column.
 //
 //   warps 0, 2  TMA producers: per k block 128 activation rows (warp 0) and this CTA's
 //               weight rows (warp 2), 128 bytes wide (128-byte swizzle), into a ring of
@@ -16,8 +15,8 @@
 //   warps 1, 3  MMA issuers (one thread each, for even and odd k blocks): four tcgen05.mma
 //               (K = 32) per k block, the first overwriting the buffer; a commit frees the
 //               stage and publishes the buffer.
-//   warps 4..11 promotion: tcgen05.ld of the buffer (four warps per 32-lane quadrant pair,
-//               each half of the columns), FP32 accumulation in registers, output.
+//   warps 4..11 promotion: tcgen05.ld of the buffer (two warps per quadrant of 32 lanes, each
+//               half of the columns), FP32 accumulation in registers, output.
 //
 // CG = 2 runs a CTA pair (cta_group::2): M = 256, each CTA holding 128 activation rows and
 // half of the weight rows, so a CTA fetches 32 KiB per 256 x 256 x 128 step instead of the 48
@@ -42,7 +41,7 @@ namespace chord {
 namespace {
 
 constexpr int kPromoteWarps = 8;
-constexpr int kFirstPromoteWarp = 4;           // a warpgroup of its own for the producer and the MMA issuer
+constexpr int kFirstPromoteWarp = 4;           // the producers and MMA issuers fill a warpgroup
 constexpr int kTileThreads = 32 * (kFirstPromoteWarp + kPromoteWarps);
 constexpr int kChunkCols = 16;                 // columns of a tensor-memory load
 constexpr int kBM = 128;                       // activation rows of a CTA
@@ -132,13 +131,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using Cfg = TileCfg<CG, BN>;
   constexpr int S = Cfg::kStages, COLS = Cfg::kCols, B = Cfg::kBufs;
   static_assert(EPI == kRows || (CG == 2 && BN == 256), "the gate_up tile");
+  static_assert(S >= B, "a stage's barrier must not complete twice before its product is read");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [S] stage loaded (rank 0's is used)
   uint64_t* done = full + S;                           // [S] stage multiplied: it may be refilled, its
-                                                       // product read (one commit a block: each holds a
-                                                       // pair's MMAs up by about 400 cycles)
+                                                       // product read
   uint64_t* acc_empty = done + S;                      // [B] buffer read by every warp (rank 0's is used)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + B);
   __shared__ int abort_flag;
@@ -154,9 +153,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&done[s], 1);
     }
-    for (int b = 0; b < B; ++b) {
-      mbar_init(&acc_empty[b], kPromoteWarps * CG);
-    }
+    for (int b = 0; b < B; ++b) mbar_init(&acc_empty[b], kPromoteWarps * CG);
     fence_barrier_init();
   }
   __syncthreads();
