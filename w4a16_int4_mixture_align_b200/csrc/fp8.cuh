@@ -34,7 +34,6 @@ struct Fp8Args {
   const int32_t* block_row0;  // row of each unit's first position
   const int32_t* ntp;         // units * bm
   int bm;
-  int bn;                     // tile kernel: columns of a tile (256 with bm = 256)
   uint32_t* status;
   int num_sms;
   float* out_scales;  // gate_up: scales of the codes in `out`
@@ -94,7 +93,7 @@ constexpr int kFp8StreamCtas = 2;  // resident per SM
 cudaError_t launch_fp8_stream(const Fp8Args& a, int split, cudaStream_t stream);
 // Dense gate_up as launch_fp8_tile_gate_up; clusters of 2 x split CTAs, split <= 4.
 cudaError_t launch_fp8_stream_gate_up(const Fp8Args& a, int split, cudaStream_t stream);
-// (a.bm, a.bn) of (128, 128), (128, 256): single CTAs; (256, 256): CTA pairs.
+// a.bm = 128: single CTAs with tiles of 128 x 128; 256: CTA pairs, 256 x 256.
 cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream);
 // Dense, w = [gate; up] with a.N = 2 I: SiLU(gate) * up quantised to q [rows, I], scales [I/128, rows].
 cudaError_t launch_fp8_tile_gate_up(const Fp8Args& a, cudaStream_t stream);

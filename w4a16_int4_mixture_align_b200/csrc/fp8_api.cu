@@ -88,7 +88,6 @@ constexpr double kStreamStart[3] = {4.6, 5.0, 6.4}, kStreamPerKb[3] = {0.37, 0.3
 struct Plan {
   bool tensor;  // the tile kernel (fp8_tile.cu) or the streaming one (fp8_stream.cu)
   int bm;       // rows of a unit
-  int bn;       // columns of a tile
   int split;    // streaming: CTAs that share an item
   double us;    // estimate
 };
@@ -97,12 +96,11 @@ struct Plan {
 // wave of the CTAs, the k blocks of an item times a time per block (and a time per tile),
 // fitted to measurements on a B200 over M = 8 .. 4096 of 4096 x 7168, 7168 x 2048, 512 x 7168,
 // 576 x 1520 and 7168 x 256 (N x K); it lies within a quarter of them. On both sides of some
-// borders, in us, for 64-row streaming, 128 x 128, 128 x 256 and 256 x 256 tiles: 4096 x 7168
-// M=128 14.0, 18.0, 29.3, 29.8; M=512 35.5, 19.9, 31.0, 31.3; M=1024 -, 36.0, 32.1, 32.6; M=4096
-// -, 170, 123, 122; 512 x 7168 M=512 11.5, 17.7, 29.1, 29.0; 7168 x 2048 M=512 25, 13.9, 13.3, 13.5.
-// 48 experts of 7168 x 2048 with two blocks each (contiguous): 209 us by 256 x 256 tiles, 222 by
-// 128 x 256, 277 by 128 x 128. `expected`: rows per expert; masked experts are taken to hold up
-// to 1.25 times as many.
+// borders, in us, for 64-row streaming, 128 x 128 and 256 x 256 tiles: 4096 x 7168 M=128 14.3,
+// 17.5, 29.1; M=512 35.3, 19.0, 29.5; M=1024 -, 33.8, 31.0; M=4096 -, 121, 115; 512 x 7168 M=512
+// 12.1, 17.4, 28.6; 7168 x 2048 M=512 26, 12.9, 13.0. 48 experts (contiguous) of 7168 x 2048 with
+// one block each 216, 145, 203, two 482, 240, 211. `expected`: rows per expert; masked experts
+// are taken to hold up to 1.25 times as many.
 Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
   const int KB = fp8_blocks(a.K);
   // contiguous: every 128-row block is a unit, or several; pairs of an expert's blocks are units
@@ -117,8 +115,8 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
   auto waves = [](int64_t items, int64_t slots) { return double((items + slots - 1) / slots); };
   Plan best{};
   best.us = 1e30;
-  auto offer = [&](bool tensor, int bm, int bn, int split, double us) {
-    if (us < best.us) best = Plan{tensor, bm, bn, split, us};
+  auto offer = [&](bool tensor, int bm, int split, double us) {
+    if (us < best.us) best = Plan{tensor, bm, split, us};
   };
   if (!(flags & CHORD_FLAG_FORCE_TENSOR)) {
     const int64_t slots = int64_t(a.num_sms) * kFp8StreamCtas, tiles = (a.N + 127) / 128;
@@ -129,15 +127,13 @@ Plan choose_plan(const Fp8Args& a, int64_t expected, int flags) {
       // a split grid covers every unit there may be, so it has to stay small
       const int64_t most = ((a.rows + bm - 1) / bm + (a.layout == kFp8Dense ? 0 : a.E)) * tiles;
       if (most * split > 8 * slots) split = 1;
-      offer(false, bm, 128, split, kStreamStart[i] + waves(items * split, slots) * ((KB + split - 1) / split) * kStreamPerKb[i]);
+      offer(false, bm, split, kStreamStart[i] + waves(items * split, slots) * ((KB + split - 1) / split) * kStreamPerKb[i]);
     }
   }
   if (!(flags & CHORD_FLAG_FORCE_STREAM)) {
-    // (many waves of small tiles wait for L2)
     const double small = waves(units_of(128) * ((a.N + 127) / 128), a.num_sms);
-    offer(true, 128, 128, 1, 2.6 + small * (KB * (small > 3 ? 0.32 : 0.265) + 1.4));
-    offer(true, 256, 256, 1, 3.0 + waves(units_of(256) * ((a.N + 255) / 256), a.num_sms / 2) * (KB * 0.50 + 0.9));
-    offer(true, 128, 256, 1, 3.0 + waves(units_of(128) * ((a.N + 255) / 256), a.num_sms) * (KB * 0.53 + 0.9));
+    offer(true, 128, 1, 2.6 + small * (KB * (small > 3 ? 0.275 : 0.265) + 1.4));
+    offer(true, 256, 1, 3.0 + waves(units_of(256) * ((a.N + 255) / 256), a.num_sms / 2) * (KB * 0.485 + 0.9));
   }
   return best;
 }
@@ -149,7 +145,6 @@ chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices
   const Plan plan = choose_plan(a, expected, flags);
   const bool tensor = plan.tensor;
   a.bm = plan.bm;
-  a.bn = plan.bn;
   cudaError_t err;
   if (a.layout != kFp8Dense) {
     const Fp8Workspace ws = fp8_workspace(a.rows, a.E);
@@ -172,8 +167,8 @@ chord_status_t run_product(Fp8Args a, int64_t expected, const int32_t* m_indices
 
 // The same for gate_up (a.N = 2 I): streaming by clusters of 2 x split CTAs or 256-row x 128-column
 // tiles, both ending in the quantised SiLU(gate) * up; or, for up to kTwoStepRows rows (split = 0),
-// the product in FP32 and a quantisation. In us for 4096 x 7168: M=16 9.8, 33.3, 12.1; M=128
-// 15.3, 33.6, 19.6; M=512 -, 34.9, 29.1; M=1024 -, 36.1, 41.4.
+// the product in FP32 and a quantisation. In us for 4096 x 7168: M=16 9.6, 31.9, 11.7; M=128
+// 15.3, 32.1, 19.2; M=512 -, 33.2, 26.7; M=1024 -, 34.8, 39.4.
 constexpr int64_t kTwoStepRows = 1024;
 Plan choose_gate_up(const Fp8Args& a, int flags) {
   const int KB = fp8_blocks(a.K);
@@ -187,17 +182,17 @@ Plan choose_gate_up(const Fp8Args& a, int flags) {
       const int most = stream_split(2 * items, KB, slots), split = most < 4 ? most : 4;
       const double us = kStreamStart[i] + 1.0 +
                         double((2 * items * split + slots - 1) / slots) * ((KB + split - 1) / split) * kStreamPerKb[i];
-      if (us < best.us) best = Plan{false, bm, 128, split, us};
+      if (us < best.us) best = Plan{false, bm, split, us};
     }
   }
   if (!(flags & CHORD_FLAG_FORCE_STREAM)) {
     const int64_t tiles = (a.rows + 255) / 256 * (a.N / 256), pairs = a.num_sms / 2;
-    const double us = 3.0 + double((tiles + pairs - 1) / pairs) * (KB * 0.50 + 2.0);
-    if (us < best.us) best = Plan{true, 256, 256, 1, us};
+    const double us = 3.0 + double((tiles + pairs - 1) / pairs) * (KB * 0.485 + 2.0);
+    if (us < best.us) best = Plan{true, 256, 1, us};
   }
   if (!(flags & (CHORD_FLAG_FORCE_TENSOR | CHORD_FLAG_FORCE_STREAM)) && a.rows <= kTwoStepRows) {
     const double us = choose_plan(a, a.rows, flags).us + 4.5 + double(a.rows) * a.N * 8 / 5e6;
-    if (us < best.us) best = Plan{false, 0, 0, 0, us};
+    if (us < best.us) best = Plan{false, 0, 0, us};
   }
   return best;
 }
@@ -349,7 +344,6 @@ chord_status_t chord_fp8_gate_up(const uint8_t* xq, const float* xs, int64_t M, 
   }
   a.out_scales = scales;
   a.bm = plan.bm;
-  a.bn = plan.bn;
   const cudaError_t err = plan.tensor ? launch_fp8_tile_gate_up(a, cs) : launch_fp8_stream_gate_up(a, plan.split, cs);
   return err == cudaSuccess ? CHORD_OK : cuda_fail(err, "FP8 gate_up launch");
 }

@@ -9,27 +9,33 @@
 // Activation rows are the M side, so a thread owns one row and a block costs it one scale and
 // one fused multiply-add per column.
 //
-//   warps 0, 2  TMA producers: per k block 128 activation rows (warp 0) and this CTA's
-//               weight rows (warp 2), 128 bytes wide (128-byte swizzle), into a ring of
-//               stages.
+//   warp 0      TMA producer: per k block 128 activation rows and this CTA's weight rows, 128
+//               bytes wide (128-byte swizzle), into a ring of stages.
+//   warp 2      the same k blocks' scales into a ring in shared memory, by 4-byte asynchronous
+//               copies; a stage counts as full with them.
 //   warps 1, 3  MMA issuers (one thread each, for even and odd k blocks): four tcgen05.mma
 //               (K = 32) per k block, the first overwriting the buffer; a commit frees the
 //               stage and publishes the buffer.
 //   warps 4..11 promotion: tcgen05.ld of the buffer (two warps per quadrant of 32 lanes, each
 //               half of the columns), FP32 accumulation in registers, output.
 //
-// CG = 2 runs a CTA pair (cta_group::2): M = 256, each CTA holding 128 activation rows and
-// half of the weight rows, so a CTA fetches 32 KiB per 256 x 256 x 128 step instead of the 48
-// of a single 128 x 256 tile. At 8192 x 4096 x 7168 (M x N x K) the pairs take 220 us and the
-// single tiles 228, at 4096 rows 121 and 122; the single ones serve units of 128 rows. 128 x
-// 128 tiles serve products of few tiles (512 rows: 20 us against 31).
+// The promotion warps load nothing from global memory while they add: a wait for a tensor-memory
+// load lasts until the warp's other loads in flight are back as well, 1000 cycles and more
+// under the kernel's own traffic. With scales loaded to registers (two k blocks ahead) 4096 x
+// 4096 x 7168 (M x N x K) takes 124 us, with the ring 114.
 //
-// Bound: the round trip of a tensor-memory buffer. Measured in cycles, a block's MMAs take
-// 660 (an instruction of K = 32 takes 130 to 165 whatever its N), their end is seen 340
-// later, reading the buffer takes 440 and handing it back 500; with two buffers that is about
-// 1000 a block, 2.2 PFLOP/s. Tiles of 128 columns have four buffers and run at their MMAs'
-// pace, 520 for half the work. The TMA feed alone would allow 660 (3.2 PFLOP/s while operands
-// stay in L2), the FP32 additions 256.
+// CG = 2 runs a CTA pair (cta_group::2): M = 256, each CTA holding 128 activation rows and
+// half of the weight rows: 32 KiB per 256 x 256 x 128 step and CTA. Single CTAs with 128 x 128
+// tiles serve products of few tiles (512 x 4096 x 7168: 19 us against 29) and experts of one
+// block (48 of 7168 x 2048: 145 us against 203; 128 x 256 tiles 149).
+//
+// Bound: the round trip of a tensor-memory buffer. A block's four MMAs take 512 cycles (a K of
+// 32 takes 128 at N = 256, 64 at N = 128), their end is seen about 200 later, reading the buffer
+// and adding half of it takes 250 (the additions alone keep the FP32 pipe busy for 256 a block),
+// handing it back 250; two buffers of 256 columns fill tensor memory, so a block takes about
+// 780, 2.3 PFLOP/s at 8192 x 4096 x 7168 (212 us). Neither MMAs of one column half each with
+// four buffers (same time) nor sixteen promotion warps (260 us) nor the whole reading by halves
+// of 32-column loads (spills, 249 us) shorten it. The TMA feed runs 6000 cycles ahead.
 //
 // All waits are bounded. On a timeout a CTA raises CHORD_DEV_TIMEOUT, waits (bounded) for
 // its copies and MMAs in flight, frees its tensor memory and returns.
@@ -43,22 +49,26 @@ namespace {
 constexpr int kPromoteWarps = 8;
 constexpr int kFirstPromoteWarp = 4;           // the producers and MMA issuers fill a warpgroup
 constexpr int kTileThreads = 32 * (kFirstPromoteWarp + kPromoteWarps);
-constexpr int kChunkCols = 16;                 // columns of a tensor-memory load
 constexpr int kBM = 128;                       // activation rows of a CTA
 constexpr int kABytes = kBM * kFp8Block;
 constexpr int kFixedBytes = 1024;              // barriers and the TMEM slot
 constexpr int kStagingBytes = 4096;            // output staging of a promotion warp
 constexpr int kOutBytes = kPromoteWarps * kStagingBytes;
+constexpr int kScaleBytes = 4 * (kBM + 4);     // scales of a k block: 128 rows', two column blocks'
+constexpr int kScaleLag = 2;                   // k blocks of scales on their way (1 and 2 take the same)
 constexpr int kSmemBudget = 232448 - 1024 - kFixedBytes - kOutBytes;  // 227 KiB less alignment slack
 
 template <int CG, int BN>
 struct TileCfg {
   static constexpr int kBRows = BN / CG;
   static constexpr int kStageBytes = kABytes + kBRows * kFp8Block;
-  static constexpr int kStages = kSmemBudget / kStageBytes > 8 ? 8 : kSmemBudget / kStageBytes;
-  static constexpr int kSmemBytes = 1024 + kFixedBytes + kStages * kStageBytes + kOutBytes;
-  static constexpr int kCols = BN / 2;         // columns of a promotion warp
   static constexpr int kBufs = 512 / BN;       // tensor-memory buffers
+  static constexpr int kStages = (kSmemBudget - (8 + kBufs) * kScaleBytes) / kStageBytes;
+  static constexpr int kScaleSlots = kStages + kBufs;
+  static constexpr int kSmemBytes = 1024 + kFixedBytes + kStages * kStageBytes + kOutBytes + kScaleSlots * kScaleBytes;
+  static constexpr int kCols = BN / 2;         // columns of a promotion warp
+  static constexpr int kChunk = BN == 128 ? 32 : 16;       // columns of a tensor-memory load: two of
+                                                           // 32 would spill behind 128 sums
 };
 
 // Registers per thread: 384 threads launch with 168 each (64512 together); the 256 promotion
@@ -75,6 +85,22 @@ __device__ __forceinline__ void give_registers() {
 struct TileMaps {
   CUtensorMap x, w, out;
 };
+
+// Four bytes to shared memory without a register in between.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but this thread's last N groups have landed.
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float lds_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -129,8 +155,9 @@ template <int CG, int BN, int EPI>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fp8_tile_kernel(const __grid_constant__ TileMaps maps, const Fp8Args p) {
   using Cfg = TileCfg<CG, BN>;
-  constexpr int S = Cfg::kStages, COLS = Cfg::kCols, B = Cfg::kBufs;
+  constexpr int S = Cfg::kStages, COLS = Cfg::kCols, B = Cfg::kBufs, D = Cfg::kScaleSlots;
   static_assert(EPI == kRows || (CG == 2 && BN == 256), "the gate_up tile");
+  static_assert(S <= 8 && S > kScaleLag, "ring");
   static_assert(S >= B, "a stage's barrier must not complete twice before its product is read");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -147,10 +174,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const uint32_t scales = sbase + kFixedBytes + S * Cfg::kStageBytes + kOutBytes;  // [D] slots
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + CG);  // the copies and each CTA's scales
       mbar_init(&done[s], 1);
     }
     for (int b = 0; b < B; ++b) mbar_init(&acc_empty[b], kPromoteWarps * CG);
@@ -176,39 +204,84 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp < kFirstPromoteWarp) {
     give_registers<40>();
-    if (warp == 0 || warp == 2) {
-      // warp 0 copies activation rows, warp 2 weight rows
+    const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : smem_u32(full);
+    if (warp == 0) {
       if (lane == 0) {
-        const bool of_x = warp == 0;
-        const CUtensorMap* map = of_x ? &maps.x : &maps.w;
-        const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : smem_u32(full);
-        const uint32_t dst = sbase + kFixedBytes + (of_x ? 0 : kABytes);
         uint32_t fill = 0;
         bool ok = true;
         for (int t = cid; t < tiles && ok; t += ncl) {
           const int u = t / NT, nt = t - u * NT;
-          int row;
-          if (of_x) row = (p.layout == kFp8Dense ? u * kBM * CG : __ldcg(p.block_row0 + u)) + int(rank) * kBM;
-          else if (EPI == kGateUp) row = int(rank) * I + nt * kFp8Block;
-          else row = (p.layout == kFp8Dense ? 0 : __ldcg(p.expert_ids + u)) * p.N + nt * BN + int(rank) * Cfg::kBRows;
+          const int xrow = (p.layout == kFp8Dense ? u * kBM * CG : __ldcg(p.block_row0 + u)) + int(rank) * kBM;
+          int wrow;
+          if (EPI == kGateUp) wrow = int(rank) * I + nt * kFp8Block;
+          else wrow = (p.layout == kFp8Dense ? 0 : __ldcg(p.expert_ids + u)) * p.N + nt * BN + int(rank) * Cfg::kBRows;
           for (int kb = 0; kb < KB; ++kb, ++fill) {
             const uint32_t s = fill % S;
             if (fill >= S && !mbar_wait(&done[s], ((fill / S) - 1) & 1, abort_v, p.status)) {
               ok = false;
               break;
             }
-            if (rank == 0 && of_x) mbar_arrive_expect_tx(&full[s], CG * Cfg::kStageBytes);
-            tma_2d<CG>(dst + s * Cfg::kStageBytes, map, kb * kFp8Block, row, full0 + s * 8);
+            const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes, bar = full0 + s * 8;
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * Cfg::kStageBytes);
+            tma_2d<CG>(st, &maps.x, kb * kFp8Block, xrow, bar);
+            tma_2d<CG>(st + kABytes, &maps.w, kb * kFp8Block, wrow, bar);
           }
         }
         // the last copies have landed before the CTA ends (rank 0's barriers count both CTAs')
-        if (rank == 0 && of_x) {
+        if (rank == 0) {
           int dummy = 0;
           for (uint32_t f = fill > S ? fill - S : 0; f < fill; ++f)
             mbar_wait(&full[f % S], (f / S) & 1, &dummy, p.status);
         }
       }
       __syncwarp();
+    } else if (warp == 2) {
+      // scales of the k blocks into a ring of D = S + B slots: a stage is filled again once its
+      // product is formed, which took the buffer of B blocks before it, whose scales had been read
+      uint32_t fill = 0, told = 0;
+      bool ok = true;
+      auto tell = [&] {  // the oldest block's scales are there
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2) mbar_arrive_cluster(full0 + told % S * 8);
+          else mbar_arrive(&full[told % S]);
+        }
+        ++told;
+      };
+      for (int t = cid; t < tiles && ok; t += ncl) {
+        const int u = t / NT, nt = t - u * NT;
+        const int row0 = (p.layout == kFp8Dense ? u * kBM * CG : __ldcg(p.block_row0 + u)) + int(rank) * kBM;
+        const int e = p.layout == kFp8Dense ? 0 : __ldcg(p.expert_ids + u);
+        const float* xs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = row0 + 32 * i + lane;
+          xs[i] = p.xs + (row < p.rows ? row : 0);  // rows that are not stored read row 0's
+        }
+        // lanes 0 and 1: of the two halves of the columns (kGateUp: gate, up)
+        const int nb = EPI == kGateUp ? nt + (lane & 1) * (I / kFp8Block) : min((nt * BN + (lane & 1) * COLS) / kFp8Block, NB - 1);
+        const float* ws = p.ws + (int64_t(e) * NB + nb) * KB;
+        for (int kb = 0; kb < KB; ++kb, ++fill) {
+          if (fill >= S && !mbar_wait_warp(&done[fill % S], ((fill / S) - 1) & 1, abort_v, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = scales + fill % D * kScaleBytes + 4 * lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            copy_async4(dst + 128 * i, xs[i]);
+            xs[i] += p.rows;
+          }
+          if (lane < 2) copy_async4(dst + 4 * kBM, ws + kb);
+          copy_async_commit();
+          if (fill - told >= kScaleLag) {
+            copy_async_wait<kScaleLag>();
+            tell();
+          }
+        }
+      }
+      copy_async_wait<0>();
+      while (told < fill) tell();
     } else if (lane == 0 && rank == 0) {
       // warp 1 multiplies the even k blocks, warp 3 the odd ones: issuing a block's MMAs holds
       // its thread for about their time, so a single issuer's waits and commits between two
@@ -242,7 +315,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t empty0 = CG == 2 ? cluster_addr(acc_empty, 0) : smem_u32(acc_empty);
     const uint32_t src = tmem + (uint32_t(q * 32) << 16) + (EPI == kGateUp ? h * 64 : h * COLS);
     // column (from src) of chunk c: a kGateUp warp's second half are the up columns
-    auto chunk = [](int c) { return EPI == kGateUp && c >= 64 / kChunkCols ? 128 + kChunkCols * c - 64 : kChunkCols * c; };
+    auto chunk = [](int c) { return EPI == kGateUp && c >= 64 / Cfg::kChunk ? 128 + Cfg::kChunk * c - 64 : Cfg::kChunk * c; };
     const uint32_t staging = sbase + kFixedBytes + S * Cfg::kStageBytes + (warp - kFirstPromoteWarp) * kStagingBytes;
     uint32_t it = 0;
     bool ok = true;
@@ -250,72 +323,53 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int t = cid; t < tiles && (ok || EPI == kGateUp); t += ncl) {
       const int u = t / NT;
       const int n0 = EPI == kGateUp ? (t - u * NT) * kFp8Block + h * 64 : (t - u * NT) * BN + h * COLS;
-      const int e = p.layout == kFp8Dense ? 0 : __ldcg(p.expert_ids + u);
       const int pos = u * kBM * CG + int(rank) * kBM + r;
       const int64_t row = p.layout == kFp8Dense ? pos : __ldcg(p.block_row0 + u) + int(rank) * kBM + r;
       const bool live = p.layout == kFp8Dense ? row < p.rows : __ldcg(p.sorted_ids + pos) >= 0;
-      // scales: one per row (rows that are not stored read row 0's), one for the columns
-      const float* xs = p.xs + (row < p.rows ? row : 0);
-      const int nb = min(n0 / kFp8Block, NB - 1);
-      const float* ws = p.ws + (int64_t(e) * NB + nb) * KB;
-      const float* wu = EPI == kGateUp ? ws + int64_t(I / kFp8Block) * KB : ws;  // of the up columns
       uint64_t sum[COLS / 2];  // columns 2i, 2i + 1
 #pragma unroll
       for (int c = 0; c < COLS / 2; ++c) sum[c] = 0;
-      // the scales of this k block and the next two (loads run two blocks ahead)
-      float x0 = __ldcg(xs), w0 = __ldcg(ws), x1 = 0.f, w1 = 0.f;
-      float u0 = EPI == kGateUp ? __ldcg(wu) : 0.f, u1 = 0.f;
-      if (KB > 1) {
-        xs += p.rows;
-        x1 = __ldcg(xs);
-        w1 = __ldcg(ws + 1);
-        if (EPI == kGateUp) u1 = __ldcg(wu + 1);
-      }
-      // the tensor-memory loads run one chunk of columns ahead of the additions, across k
-      // blocks too
-      constexpr int W = kChunkCols, CH = COLS / W;
-      uint32_t v[2][W];
-      ok = mbar_wait_warp(&done[it % S], (it / S) & 1, abort_v, p.status);
-      tc_fence_after();
-      tmem_ld_async(src + (it % B) * BN, v[0]);
+      // half of the columns at a time: the second half is in registers, and the buffer handed
+      // back, before it is added
+      constexpr int W = Cfg::kChunk, CH = COLS / W / 2;
+      uint32_t v[CH][W];
 #pragma unroll 1
       for (int kb = 0; kb < KB; ++kb) {
-        const uint64_t s = pack2(x0 * w0, x0 * w0), s_up = EPI == kGateUp ? pack2(x0 * u0, x0 * u0) : s;
-        x0 = x1;
-        w0 = w1;
-        u0 = u1;
-        if (kb + 2 < KB) {
-          xs += p.rows;
-          x1 = __ldcg(xs);
-          w1 = __ldcg(ws + kb + 2);
-          if (EPI == kGateUp) u1 = __ldcg(wu + kb + 2);
-        }
-        const uint32_t b = it % B;
+        ok = mbar_wait_warp(&done[it % S], (it / S) & 1, abort_v, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t b = it % B, slot = scales + it % D * kScaleBytes;
         ++it;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          tmem_wait_ld(v[c & 1]);
-          if (c + 1 < CH) {
-            tmem_ld_async(src + b * BN + chunk(c + 1), v[(c + 1) & 1]);
-          } else {  // the buffer is read: hand it back, and request the next one's first chunk
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (CG == 2) mbar_arrive_cluster(empty0 + b * 8);
-              else mbar_arrive(&acc_empty[b]);
-            }
-            if (kb + 1 < KB) ok = ok && mbar_wait_warp(&done[it % S], (it / S) & 1, abort_v, p.status);
-            tc_fence_after();
-            // after the last block this rereads a buffer of this CTA, for nothing
-            tmem_ld_async(src + (it % B) * BN, v[0]);
-          }
-#pragma unroll
-          for (int j = 0; j < W; j += 2)
-            fma2(sum[(W * c + j) / 2], v[c & 1][j], v[c & 1][j + 1], W * c >= COLS / 2 ? s_up : s);
+        for (int c = 0; c < CH; ++c) tmem_ld_async(src + b * BN + chunk(c), v[c]);
+        const float x = lds_f32(slot + 4 * r), w0 = lds_f32(slot + 4 * kBM + (EPI == kGateUp ? 0 : 4 * h));
+        const uint64_t s = pack2(x * w0, x * w0);
+        uint64_t s_up = s;
+        if (EPI == kGateUp) {
+          const float w1 = lds_f32(slot + 4 * kBM + 4);
+          s_up = pack2(x * w1, x * w1);
         }
-        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          tmem_wait_ld(v[c]);
+#pragma unroll
+          for (int j = 0; j < W; j += 2) fma2(sum[(W * c + j) / 2], v[c][j], v[c][j + 1], s);
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) tmem_ld_async(src + b * BN + chunk(CH + c), v[c]);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) tmem_wait_ld(v[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2) mbar_arrive_cluster(empty0 + b * 8);
+          else mbar_arrive(&acc_empty[b]);
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < W; j += 2) fma2(sum[(W * (CH + c) + j) / 2], v[c][j], v[c][j + 1], s_up);
       }
-      tmem_wait_ld(v[0]);
       if (!ok && EPI != kGateUp) continue;
       float acc[COLS];
 #pragma unroll
@@ -452,7 +506,7 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t stream) {
 
 cudaError_t launch_fp8_tile(const Fp8Args& a, cudaStream_t stream) {
   if (a.bm == 256) return launch<2, 256, kRows>(a, stream);
-  return a.bn == 256 ? launch<1, 256, kRows>(a, stream) : launch<1, 128, kRows>(a, stream);
+  return launch<1, 128, kRows>(a, stream);
 }
 
 cudaError_t launch_fp8_tile_gate_up(const Fp8Args& a, cudaStream_t stream) {
