@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr int S = Cfg::kStages, COLS = Cfg::kCols, B = Cfg::kBufs, D = Cfg::kScaleSlots;
   static_assert(EPI == kRows || (CG == 2 && BN == 256), "the gate_up tile");
   static_assert(S <= 8 && S > kScaleLag, "ring");
-  static_assert(S >= B, "a stage's barrier must not complete twice before its product is read");
+  static_assert(S >= B, "a stage's barriers must not be a phase behind: done for the adding warps, full for the issuers");
+  static_assert(B % 2 == 0, "a buffer belongs to one issuer");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
@@ -291,8 +292,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint32_t it = warp == 1 ? 0 : 1;
       for (; it < blocks; it += 2) {
         const uint32_t s = it % S, b = it % B;
-        if (!mbar_wait(&full[s], (it / S) & 1, abort_v, p.status) ||
-            (it >= B && !mbar_wait(&acc_empty[b], ((it / B) - 1) & 1, abort_v, p.status)))
+        // The buffer first, then the stage. A wait sees the parity of a phase only, and where S is
+        // odd a stage changes hands between the issuers, so this one may never have waited for the
+        // phase of block it - S: while that copy was still under way, a wait for the phase of block
+        // `it` would pass at once. That block it - B has been added says that it - S <= it - B landed.
+        if ((it >= B && !mbar_wait(&acc_empty[b], ((it / B) - 1) & 1, abort_v, p.status)) ||
+            !mbar_wait(&full[s], (it / S) & 1, abort_v, p.status))
           break;
         tc_fence_after();
         const uint32_t st = sbase + kFixedBytes + s * Cfg::kStageBytes;
