@@ -343,6 +343,7 @@ def _fp8_out(out, rows, N, flags):
     if out.dtype == torch.float32:
         return _ptr(out), flags | CHORD_FLAG_OUTPUT_FP32
     assert out.dtype == torch.bfloat16, f"out must be bf16 or fp32, not {out.dtype}"
+    assert not flags & CHORD_FLAG_OUTPUT_FP32, "CHORD_FLAG_OUTPUT_FP32 needs an fp32 out, not bf16"
     return _ptr(out), flags
 
 
@@ -662,7 +663,8 @@ class ChordFP8MLP:
         w13, s13, w2, s2, xq, xs, aq, a_s, ws, ws_bytes = self._pointers
         lib_, s = lib(), _stream()
         _check(lib_.chord_fp8_quantize(x_ptr, _DTYPES[x.dtype], x_ld, T, self.H, None, 0, xq, xs, s), "chord_fp8_quantize")
-        _check(lib_.chord_fp8_gate_up(xq, xs, T, self.H, w13, s13, self.I, aq, a_s, ws, ws_bytes, flags, s),
+        _check(lib_.chord_fp8_gate_up(xq, xs, T, self.H, w13, s13, self.I, aq, a_s, ws, ws_bytes,
+                                      flags & ~CHORD_FLAG_OUTPUT_FP32, s),
                "chord_fp8_gate_up")
         _check(lib_.chord_fp8_gemm(aq, a_s, T, self.I, w2, s2, self.H, out_ptr, ws, ws_bytes, down_flags, s),
                "chord_fp8_gemm")
