@@ -581,9 +581,13 @@ class ChordMoE:
         return topk_ids, topk_weights
 
     def forward_logits(self, hidden, logits, out=None, flags=0, **scoring):
-        """The layer from gate logits: route() and forward in one. Returns (out, topk_ids,
-        topk_weights)."""
+        """The layer from gate logits (a row for each row of hidden): route() and forward in one.
+        Returns (out, topk_ids, topk_weights)."""
+        assert hidden.shape == (logits.shape[0], self.H), \
+            f"hidden has shape {tuple(hidden.shape)}, needs {(logits.shape[0], self.H)}"
         topk_ids, topk_weights = self.route(logits, **scoring)
+        assert topk_ids.dim() == 2 and topk_ids.shape[1] == self.topk, \
+            f"topk_ids has shape {tuple(topk_ids.shape)}, needs {self.topk} columns"
         return self._forward_sorted(hidden, topk_ids, topk_weights, out, flags), topk_ids, topk_weights
 
     def forward(self, hidden, topk_ids, topk_weights, out=None, flags=0):
