@@ -40,3 +40,28 @@ def test_ids_of_another_width(chord):
     layer._forward_sorted = reached
     with pytest.raises(AssertionError, match="topk_ids"):
         layer.forward_logits(torch.zeros((4, 256)), torch.zeros((4, 8)), topk_ids=ids, topk_weights=w)
+
+
+def sums(chord, out, flags):
+    """forward_logits with a forward that only notes its output."""
+    import torch
+    layer = bare_layer(chord, lambda logits: (torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2))))
+    layer.device, layer.block_m, layer.I = torch.device("cpu"), 8, 128
+    layer.sorted_ids = layer.expert_ids = layer.ntp = layer.w13 = layer.w2 = layer.workspace = None
+    return layer.forward_logits(torch.zeros((4, 256)), torch.zeros((4, 8)), out=out, flags=flags)[0]
+
+
+def test_output_is_as_large_as_the_flag_makes_it(chord, monkeypatch):
+    """CHORD_FLAG_OUTPUT_FP32 writes four bytes an element: into an fp32 tensor of its own, or into an
+    `out` that holds them."""
+    import torch
+    monkeypatch.setattr(chord, "chord_moe_forward", lambda *args, **kw: None)
+    flag = chord.CHORD_FLAG_OUTPUT_FP32
+    assert sums(chord, None, 0).dtype == torch.bfloat16 and sums(chord, None, flag).dtype == torch.float32
+    for dtype, flags in ((torch.bfloat16, 0), (torch.float32, flag)):
+        out = torch.zeros((4, 256), dtype=dtype)
+        assert sums(chord, out, flags) is out
+    with pytest.raises(AssertionError, match="out holds"):
+        sums(chord, torch.zeros((4, 256), dtype=torch.bfloat16), flag)
+    with pytest.raises(AssertionError, match="out holds"):
+        sums(chord, torch.zeros((3, 256), dtype=torch.bfloat16), 0)

@@ -598,8 +598,11 @@ class ChordMoE:
         return self._forward_sorted(hidden, topk_ids, topk_weights, out, flags)
 
     def _forward_sorted(self, hidden, topk_ids, topk_weights, out, flags):
+        size, dtype = (4, torch.float32) if flags & CHORD_FLAG_OUTPUT_FP32 else (2, torch.bfloat16)
         if out is None:
-            out = torch.empty((hidden.shape[0], self.H), dtype=torch.bfloat16, device=self.device)
+            out = torch.empty((hidden.shape[0], self.H), dtype=dtype, device=self.device)
+        need = hidden.shape[0] * self.H * size
+        assert _nbytes(out) >= need, f"out holds {_nbytes(out)} bytes, the output needs {need}"
         chord_moe_forward(hidden, topk_ids, topk_weights, self.sorted_ids, self.expert_ids, self.ntp,
                           self.block_m, self.w13, self.w2, self.I, self.E, out, self.workspace, flags)
         return out
