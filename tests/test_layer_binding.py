@@ -65,3 +65,10 @@ def test_output_is_as_large_as_the_flag_makes_it(chord, monkeypatch):
         sums(chord, torch.zeros((4, 256), dtype=torch.bfloat16), flag)
     with pytest.raises(AssertionError, match="out holds"):
         sums(chord, torch.zeros((3, 256), dtype=torch.bfloat16), 0)
+
+
+def test_one_stream_for_routing_and_forward(chord):
+    """`stream` is an argument of the router alone: the forward would not wait for it."""
+    import torch
+    with pytest.raises(TypeError, match="stream"):
+        bare_layer(chord, reached).forward_logits(torch.zeros((4, 256)), torch.zeros((4, 8)), stream=object())

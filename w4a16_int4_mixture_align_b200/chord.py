@@ -581,8 +581,10 @@ class ChordMoE:
         return topk_ids, topk_weights
 
     def forward_logits(self, hidden, logits, out=None, flags=0, **scoring):
-        """The layer from gate logits (a row for each row of hidden): route() and forward in one.
-        Returns (out, topk_ids, topk_weights)."""
+        """The layer from gate logits (a row for each row of hidden): route() and forward in one, on
+        the current stream. Returns (out, topk_ids, topk_weights)."""
+        if "stream" in scoring:  # the router's alone: the forward would not wait for it
+            raise TypeError("forward_logits takes no stream, it runs on the current one")
         assert hidden.shape == (logits.shape[0], self.H), \
             f"hidden has shape {tuple(hidden.shape)}, needs {(logits.shape[0], self.H)}"
         topk_ids, topk_weights = self.route(logits, **scoring)
