@@ -50,9 +50,14 @@ struct StreamParams {
   uint32_t* flags;          // stream-K flags [kMaxStreamWorkers][8], zero between launches
 };
 
-__device__ __forceinline__ uint4 ldg_nc128(const void* p) {
+// 16 bytes of an activation row through L1, not as read-only data: the kernel before this one, behind
+// which it is launched early, may have written the row after this one had started (the
+// intermediate of the gate_up kernel, or hidden rows that come straight from a kernel that lets
+// its successor start). The address comes from a descriptor read after the wait for that kernel,
+// so the load cannot move ahead of it.
+__device__ __forceinline__ uint4 ldg128(const void* p) {
   uint4 v;
-  asm("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 
@@ -78,7 +83,7 @@ __device__ __forceinline__ void load_tile_x(uint4 (&xv)[4][NT8], const uint16_t*
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int n8 = 0; n8 < NT8; ++n8) xv[j][n8] = ldg_nc128(xrow[n8] + off + 32 * j);
+    for (int n8 = 0; n8 < NT8; ++n8) xv[j][n8] = ldg128(xrow[n8] + off + 32 * j);
 }
 
 // Dequantises one tile for warp `rb` (16 rows) and accumulates it against the routed

@@ -19,7 +19,7 @@
 //                 stages of one item inside it) it publishes a descriptor, with the
 //                 routing metadata of the next piece already loaded. The few routed
 //                 activation rows are small and shared by every warp, so consumers read
-//                 them straight from global memory through L1 (ld.global.nc). (Copying each
+//                 them straight from global memory through L1. (Copying each
 //                 stage's activation slice into shared memory beside the weights, by the
 //                 producer's lanes with cp.async, measured slower: the producer's time per
 //                 stage is on the critical path.)
@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_gemm_kernel(StreamParams p
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
     // Launched early (programmatic launch), the gate_up kernel may start while the routing
-    // sort still runs: wait for it before reading the routing tensors. The down kernel's
+    // sort still runs: wait for it before reading the routing tensors (by ordinary loads, not
+    // as read-only data; past L1 they cost 0.4 us a call). The down kernel's
     // producer reads only those tensors (complete before the gate_up kernel passed this
     // same wait) and the weights, so it starts streaming at once; its consumers wait for
     // the intermediate a.
@@ -169,11 +170,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_gemm_kernel(StreamParams p
       const int64_t bc = div_fast(w, NTILES);
       const int64_t b = div_fast(bc, cpb);
       const int c = int(bc - b * cpb);
-      e = __ldg(p.expert_ids + b);
+      e = p.expert_ids[b];
       pos0 = int(b * p.block_m) + c * TC;
       const int lim = int(b * p.block_m) + p.block_m;
       f = -1;
-      if (lane < TC && pos0 + lane < lim) f = __ldg(p.sorted_ids + pos0 + lane);
+      if (lane < TC && pos0 + lane < lim) f = p.sorted_ids[pos0 + lane];
     };
     // the flat slot, or -1 for padding, a sentinel or an expert outside [0, E)
     auto valid_slot = [&](int e, int f) -> int {

@@ -11,7 +11,7 @@
 //                 item's tiles (codes + scales, 36 KiB: a bulk copy has a high fixed cost,
 //                 so bytes per copy decide the streaming rate). The few routed activation
 //                 rows are small and shared by every warp, so consumers read them straight
-//                 from global memory through L1 (ld.global.nc) instead of staging them.
+//                 from global memory through L1 instead of staging them.
 //   warps 1..8    consumer group 0 takes the first item of each pair, warps 9..16 group 1
 //                 the second; a warp owns 16 physical rows of each tile. Codes go shared ->
 //                 registers and dequantise to bf16 pairs (subtract 8, then scale) that are
@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_gemm_kernel(StreamParams p
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
     // Launched early (programmatic launch), the gate_up kernel may start while the routing
-    // sort still runs: wait for it before reading the routing tensors. The down kernel's
+    // sort still runs: wait for it before reading the routing tensors (by ordinary loads, not
+    // as read-only data; past L1 they cost 0.4 us a call). The down kernel's
     // producer reads only those tensors (complete before the gate_up kernel passed this
     // same wait) and the weights, so it starts streaming at once; its consumers wait for
     // the intermediate a.
@@ -137,10 +138,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_gemm_kernel(StreamParams p
       const int64_t bc = w / NGRP;
       const int64_t b = bc / cpb;
       const int c = int(bc % cpb);
-      e = __ldg(p.expert_ids + b);
+      e = p.expert_ids[b];
       pos0 = int(b * p.block_m) + c * TC;
       const int lim = int(b * p.block_m) + p.block_m;
-      if (lane < TC && pos0 + lane < lim) f = __ldg(p.sorted_ids + pos0 + lane);
+      if (lane < TC && pos0 + lane < lim) f = p.sorted_ids[pos0 + lane];
     };
     int qe[kLook], qpos[kLook], qf[kLook];
 #pragma unroll
