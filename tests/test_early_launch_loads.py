@@ -25,3 +25,13 @@ def test_routing_and_activations(name):
 def test_kernels_that_are_always_launched_early(name):
     text = source(name)
     assert "grid_dep_wait" in text and "__ldg(" not in text and "ld.global.nc" not in text
+
+
+@pytest.mark.parametrize("name", ["stream_gemm.cu", "stream_gemm_short.cu"])
+def test_no_block_ends_before_the_kernel_before_it(name):
+    """A grid that ends at once (another weight's blob) must not let its successor overtake its
+    predecessor."""
+    text = source(name)
+    before_roles = text[text.index("abort_flag = 2;"):text.index("// ---", text.index("abort_flag = 2;"))]
+    left = before_roles[before_roles.index("if (abort_flag)"):]
+    assert "grid_dep_wait();" in left[:left.index("return;")]

@@ -85,3 +85,28 @@ def test_hidden_rows_straight_from_an_fp8_product(chord, T):
     for _ in range(3):
         for got, y in zip([step(x, False) for x in xs], want):
             assert torch.equal(got, y)
+
+
+def test_mismatched_blob_behind_the_router(chord):
+    """A gate_up kernel that refuses its weights ends at once; the down kernel, whose weights are right,
+    and the next step still find the routing complete."""
+    import torch
+    from w4a16_int4_mixture_align_b200 import inputs
+    d = inputs.make_inputs(inputs.CONFIGS["tiny"])
+    E, T = d["qw13"].shape[0], 16
+    layer = chord.ChordMoE(d["qw13"], d["s13"].view(np.int16), d["qw2"], d["s2"].view(np.int16), topk=2, max_tokens=T,
+                           block_m=8)
+    g = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn((T, layer.H), generator=g, device="cuda").to(torch.bfloat16)
+    steps = [torch.randn((T, E), generator=g, device="cuda") for _ in range(8)]
+    want = [layer.forward_logits(x, logits)[0] for logits in steps]
+    right, wrong = layer.w13, layer.w2.clone()
+    got = []
+    for logits in steps:
+        layer.w13 = wrong
+        layer.forward_logits(x, logits.flip(0))
+        layer.w13 = right
+        got.append(layer.forward_logits(x, logits)[0])
+    assert layer.check_status() == chord.CHORD_DEV_BLOB_MISMATCH
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

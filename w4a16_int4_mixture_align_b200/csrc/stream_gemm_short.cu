@@ -91,7 +91,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_gemm_kernel(StreamParams p
     fence_barrier_init();
   }
   __syncthreads();
-  if (abort_flag) return;
+  if (abort_flag) {
+    grid_dep_wait();  // a grid that ends ahead of the one before it would let the next one overtake both
+    return;
+  }
   volatile int* abort_v = &abort_flag;
 
   const int KT = p.K / kTileK;
