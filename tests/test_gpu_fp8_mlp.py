@@ -27,3 +27,25 @@ def test_fp32_sums_by_flag(chord):  # noqa: F811
     for out in (None, torch.empty((9, H), dtype=torch.bfloat16, device="cuda")):
         with pytest.raises(AssertionError, match="OUTPUT_FP32"):
             mlp(x, out=out, flags=chord.CHORD_FLAG_OUTPUT_FP32)
+
+
+def test_weights_that_are_replaced(chord):  # noqa: F811
+    """A call multiplies by the weights that the layer holds then, and checks them."""
+    import torch
+    a, b, x = weights(5), weights(40), rows(6, 2)
+    other = chord.ChordFP8MLP(*b, max_tokens=6)
+    want_a, want_b = chord.ChordFP8MLP(*a, max_tokens=6)(x), other(x)
+    mlp = chord.ChordFP8MLP(*[v.clone() for v in a], max_tokens=6)
+    assert torch.equal(mlp(x), want_a)
+    mlp.w13, mlp.s13, mlp.w2, mlp.s2 = [v.clone() for v in b]
+    junk = [torch.full((2 * I * H,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(8)]  # where the old ones were
+    assert torch.equal(mlp(x), want_b)
+    mlp.w13.data, mlp.s13.data, mlp.w2.data, mlp.s2.data = [v.clone() for v in a]
+    assert torch.equal(mlp(x), want_a) and mlp.check_status() == 0
+    for name, bad in (("w13", a[0][:I].clone()), ("s13", a[1].double()), ("w2", a[2].T), ("s2", a[3].cpu())):
+        setattr(mlp, name, bad)
+        with pytest.raises(AssertionError):
+            mlp(x)
+        setattr(mlp, name, getattr(other, name))
+    assert torch.equal(mlp(x), want_b)
+    del junk

@@ -632,11 +632,17 @@ class ChordFP8MLP:
         if tuple(w2.shape) != (self.H, self.I):
             raise ValueError(f"w2 has shape {tuple(w2.shape)}, w13 {tuple(w13.shape)}")
         H, I = self.H, self.I
-        self._weights = (_fp8_codes(w13, "w13"), _fp8_scales(s13, "s13", (_blocks128(2 * I), _blocks128(H))),
-                         _fp8_codes(w2, "w2"), _fp8_scales(s2, "s2", (_blocks128(H), _blocks128(I))))
+        self._shapes = ((2 * I, H), (_blocks128(2 * I), _blocks128(H)), (H, I), (_blocks128(H), _blocks128(I)))
+        self._weights()
         self.device = w13.device
         self.max_tokens = -1
         self.reserve(max_tokens)
+
+    def _weights(self):
+        """Pointers of the weights as the layer holds them now, after a check."""
+        n13, ns13, n2, ns2 = self._shapes
+        return (_fp8_codes(self.w13, "w13", n13), _fp8_scales(self.s13, "s13", ns13), _fp8_codes(self.w2, "w2", n2),
+                _fp8_scales(self.s2, "s2", ns2))
 
     def reserve(self, T: int):
         d = self.device
@@ -651,7 +657,7 @@ class ChordFP8MLP:
         self.workspace = _alloc_bytes(need, d)
         self.workspace[:CHORD_WORKSPACE_HEADER_BYTES].zero_()
         self.max_tokens = T
-        self._pointers = (*self._weights, _ptr(self.xq), _ptr(self.xs), _ptr(self.aq), _ptr(self.as_),
+        self._pointers = (_ptr(self.xq), _ptr(self.xs), _ptr(self.aq), _ptr(self.as_),
                           _ptr(self.workspace), _nbytes(self.workspace))
 
     def forward(self, x, out=None, flags=0):
@@ -663,13 +669,14 @@ class ChordFP8MLP:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         if T == 0:
             return out
-        # the layer's own tensors were checked when they were made: the three calls take their
-        # pointers as they are, only x and out are new
+        # the layer's own buffers were checked when they were made: the three calls take their
+        # pointers as they are
         assert x.shape == (T, self.H) and x.dtype in _FP8_INPUTS, f"x must be bf16 or fp32 [T, {self.H}]"
         x_ptr, x_ld = _rows_ptr(x)
         out_ptr, down_flags = _fp8_out(out, T, self.H, flags)
-        _here(x, out, self.w13)
-        w13, s13, w2, s2, xq, xs, aq, a_s, ws, ws_bytes = self._pointers
+        w13, s13, w2, s2 = self._weights()
+        _here(x, out, self.w13, self.s13, self.w2, self.s2)
+        xq, xs, aq, a_s, ws, ws_bytes = self._pointers
         lib_, s = lib(), _stream()
         _check(lib_.chord_fp8_quantize(x_ptr, _DTYPES[x.dtype], x_ld, T, self.H, None, 0, xq, xs, s), "chord_fp8_quantize")
         _check(lib_.chord_fp8_gate_up(xq, xs, T, self.H, w13, s13, self.I, aq, a_s, ws, ws_bytes,
