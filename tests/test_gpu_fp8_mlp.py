@@ -49,3 +49,25 @@ def test_weights_that_are_replaced(chord):  # noqa: F811
         setattr(mlp, name, getattr(other, name))
     assert torch.equal(mlp(x), want_b)
     del junk
+
+
+def test_buffers_of_a_creeping_batch_stay_bounded(chord):  # noqa: F811
+    """Outgrown buffers are kept for graphs, so they must not add up to more than a few times the
+    largest; a smaller reservation keeps what is there."""
+    import torch
+    mlp = chord.ChordFP8MLP(*weights(5))
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for T in range(1, 400):
+        mlp.reserve(T)
+        assert mlp.max_tokens >= T
+    for T in (1, 399, 7, 2):
+        mlp.reserve(T)
+    held = torch.cuda.memory_allocated() - before
+    # what one layer of this many tokens allocates (512-byte granules and 64 KiB headers included)
+    one = chord.ChordFP8MLP(*weights(5), max_tokens=mlp.max_tokens)
+    own = sum(t.numel() * t.element_size() for t in (one.xq, one.xs, one.aq, one.as_, one.workspace))
+    growths = 16                                          # of a factor of 1.5 and one row at least: 1, 2, 3, 4, 6, 9, .. 474
+    assert held <= 3 * own + growths * (65536 + 32768)
+    x = rows(399, 3)
+    assert torch.equal(mlp(x), one(x)) and mlp.max_tokens < 2 * 399

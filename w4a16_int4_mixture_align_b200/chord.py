@@ -622,8 +622,9 @@ class ChordFP8MLP:
 
     w13 e4m3 [2 I, H] (gate rows first) with scales fp32 [2 I/128, H/128], w2 e4m3 [H, I] with
     scales [H/128, I/128]; the tensors are kept as they are. Buffers are sized for up to
-    ``max_tokens`` tokens and grow with a larger call. Calls (and replays of graphs) of one
-    layer share them, so they must not overlap on the GPU.
+    ``max_tokens`` tokens and grow with a larger call, by half at least; the outgrown ones stay for
+    graphs that were captured with them. Calls (and replays of graphs) of one layer share the
+    buffers, so they must not overlap on the GPU.
     """
 
     def __init__(self, w13, s13, w2, s2, max_tokens=1):
@@ -635,7 +636,7 @@ class ChordFP8MLP:
         self._shapes = ((2 * I, H), (_blocks128(2 * I), _blocks128(H)), (H, I), (_blocks128(H), _blocks128(I)))
         self._weights()
         self.device = w13.device
-        self.max_tokens = -1
+        self.max_tokens, self._kept = -1, []
         self.reserve(max_tokens)
 
     def _weights(self):
@@ -645,10 +646,15 @@ class ChordFP8MLP:
                 _fp8_scales(self.s2, "s2", ns2))
 
     def reserve(self, T: int):
+        """Room for T tokens at least."""
+        if T <= self.max_tokens:
+            return
         d = self.device
-        # a captured graph may still point to smaller buffers: they live as long as the layer
-        self._kept = getattr(self, "_kept", []) + ([self.xq, self.xs, self.aq, self.as_, self.workspace]
-                                                   if self.max_tokens >= 0 else [])
+        # a captured graph may still point to smaller buffers: they live as long as the layer, and
+        # growing by half keeps their sum below twice the present ones
+        if self.max_tokens >= 0:
+            self._kept += [self.xq, self.xs, self.aq, self.as_, self.workspace]
+        T = max(T, self.max_tokens * 3 // 2)
         self.xq = _alloc_bytes(T * self.H, d)
         self.xs = torch.empty(max(T * _blocks128(self.H), 1), dtype=torch.float32, device=d)
         self.aq = _alloc_bytes(T * self.I, d)
