@@ -71,3 +71,20 @@ def test_buffers_of_a_creeping_batch_stay_bounded(chord):  # noqa: F811
     assert held <= 3 * own + growths * (65536 + 32768)
     x = rows(399, 3)
     assert torch.equal(mlp(x), one(x)) and mlp.max_tokens < 2 * 399
+
+
+def test_status_outlives_growth(chord):  # noqa: F811
+    """An error raised by a call, or by the replay of a graph, on buffers that the layer has outgrown
+    is still reported, once."""
+    import torch
+    mlp = chord.ChordFP8MLP(*weights(5), max_tokens=2)
+    word = mlp.workspace[:4].view(torch.int32)
+    mlp(rows(50, 1))
+    word.fill_(chord.CHORD_DEV_TIMEOUT)
+    later = mlp.workspace[:4].view(torch.int32)
+    assert later.data_ptr() != word.data_ptr()
+    assert mlp.check_status() == chord.CHORD_DEV_TIMEOUT and mlp.check_status() == 0
+    word.fill_(chord.CHORD_DEV_TIMEOUT)
+    later.fill_(chord.CHORD_DEV_ROUTING_INVALID)
+    assert mlp.check_status() == chord.CHORD_DEV_TIMEOUT | chord.CHORD_DEV_ROUTING_INVALID
+    assert mlp.check_status() == 0

@@ -646,14 +646,15 @@ class ChordFP8MLP:
                 _fp8_scales(self.s2, "s2", ns2))
 
     def reserve(self, T: int):
-        """Room for T tokens at least."""
+        """Room for T tokens at least. (Before a capture, not in it: the zeroing of the new status word
+        would only run with the graph.)"""
         if T <= self.max_tokens:
             return
         d = self.device
         # a captured graph may still point to smaller buffers: they live as long as the layer, and
         # growing by half keeps their sum below twice the present ones
         if self.max_tokens >= 0:
-            self._kept += [self.xq, self.xs, self.aq, self.as_, self.workspace]
+            self._kept.append((self.xq, self.xs, self.aq, self.as_, self.workspace))
         T = max(T, self.max_tokens * 3 // 2)
         self.xq = _alloc_bytes(T * self.H, d)
         self.xs = torch.empty(max(T * _blocks128(self.H), 1), dtype=torch.float32, device=d)
@@ -695,7 +696,11 @@ class ChordFP8MLP:
     __call__ = forward
 
     def check_status(self) -> int:
-        return chord_moe_check_status(self.workspace)
+        """The status of all calls since the last check, those on outgrown buffers included."""
+        status = chord_moe_check_status(self.workspace)
+        for *_, workspace in self._kept:
+            status |= chord_moe_check_status(workspace)
+        return status
 
 
 class GroupedWeight:
