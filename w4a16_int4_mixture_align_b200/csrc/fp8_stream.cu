@@ -27,8 +27,8 @@
 // Measured: 48 experts of 4096 x 7168 with 8 rows each (1.35 GB of weights) 214 us, 6.3 TB/s; one
 // row against 4096 x 7168 (from L2) 7.5 us, of which about 4 are start and reduction.
 //
-// All waits are bounded; on a timeout the CTA raises CHORD_DEV_TIMEOUT, writes nothing more,
-// waits (bounded) for what it has in flight and returns.
+// All waits are bounded; on a timeout the CTA raises CHORD_DEV_TIMEOUT, writes nothing more (nor
+// do the others of its cluster), waits (bounded) for what it has in flight and returns.
 #include <mutex>
 
 #include "fp8_tc.cuh"
@@ -71,6 +71,10 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // kRowsOut: rows of the output. kGateUpOut: w = [gate; up] (N = 2 I); a cluster of 2 x split CTAs
@@ -290,7 +294,9 @@ __global__ void __launch_bounds__(kThreads, StreamCfg<TN>::kCtas)
   tc_fence_before();
   __syncthreads();
   if (ctas > 1) {
-    cluster_sync_all();  // every CTA's sums are in its shared memory
+    // without one CTA's sums there is no result: where one gave up, none of its cluster writes
+    if (abort_flag && int(threadIdx.x) < ctas) st_cluster_u32(cluster_addr(&abort_flag, threadIdx.x), 1u);
+    cluster_sync_all();  // every CTA's sums are in its shared memory, every flag is known
     const int j_begin = rank * TN / ctas, j_end = (rank + 1) * TN / ctas;
     if (OUT == kGateUpOut && first < items && !abort_flag) {
       // a row's 128 columns a warp, four a lane; every CTA's share requested before any is added
