@@ -15,8 +15,8 @@
 //   1. c in FP32 for every expert (lane l: experts l, l + 32, ...). Without a bias both
 //      scores grow with the logit, so the logit itself is the key and nothing rounds.
 //   2. the k-th largest of the 32 lane maxima is at most the k-th largest c, so every
-//      expert of the answer is among those with c >= that threshold minus the FP32 error
-//      bound. Typically 8 to 12 of 384 experts are; they are compacted to one per lane.
+//      expert of the answer is among those with c >= that threshold minus twice the FP32
+//      error bound. Typically 8 to 12 of 384 experts are; they are compacted to one per lane.
 //   3. one c in FP64 per lane, the rank of each by counting larger ones, and the weights.
 // Groups are scored in FP32 as well; a border between a kept and a dropped group closer
 // than the error bound, more than 32 candidates, or k > 32 take the slow way: every c in
@@ -35,8 +35,13 @@ namespace {
 
 constexpr int kRouterWarps = 8;
 constexpr unsigned kFull = 0xffffffffu;
-// |c in FP32 - c| <= 1e-6 + |c| * 2^-24 for both scores (a sum of G exponentials and one
-// division, each exponential within a few ulp); thresholds stay four times further away.
+// How far a c in FP32 may be off, with u = 2^-24. Softmax: the denominator 46 u (each exponential
+// 4 u and, where it weighs most, 5 u for its rounded argument, up to 31 + 5 additions, one
+// division), common to all experts of a token; the expert's own exponential 4 u (2 ulp; the
+// 1.173 |x| more of a large |x| come with an e^x that falls faster), its argument u, the product u:
+// 52 u = 3.1e-6 in all, times s <= 1. Sigmoid 8 u. Adding the bias rounds by u |c|. The sum of a
+// group's two best is off by 46 u (s1 + s2) + 12 u <= 58 u = 3.5e-6, as s1 + s2 <= 1. So a slack of
+// 4e-6 + 1e-6 |c| bounds each of these, and two of them a comparison of two.
 constexpr float kSlackAbs = 4e-6f, kSlackRel = 1e-6f;
 
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -81,7 +86,7 @@ __device__ __noinline__ double score64_of(int score, float l, float lmax, double
 __device__ __forceinline__ double score64(const RouterArgs& p, float l, float lmax, double rz) {
   return score64_of(p.score, l, lmax, rz);
 }
-// s in FP32, within 1e-6.
+// s in FP32, within the bound above.
 __device__ __forceinline__ float score32(const RouterArgs& p, float l, float lmax, float rz) {
   if (p.score == CHORD_SCORE_SOFTMAX) return __expf(l - lmax) * rz;
   return __fdividef(1.f, 1.f + __expf(-fminf(fmaxf(l, -80.f), 80.f)));
@@ -356,7 +361,7 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
       above += (o.x > best) + (o.y > best) + (o.z > best) + (o.w > best);
     }
     thr = warp_min(above < p.k ? best : INFINITY);
-    if (p.bias && thr > -INFINITY) thr -= kSlackAbs + kSlackRel * fabsf(thr);
+    if (p.bias && thr > -INFINITY) thr -= 2.f * (kSlackAbs + kSlackRel * fabsf(thr));
     __syncwarp();
   }
   int n = 0;
