@@ -361,7 +361,7 @@ __device__ __forceinline__ void route_token(const RouterArgs& p, int64_t t, uint
       above += (o.x > best) + (o.y > best) + (o.z > best) + (o.w > best);
     }
     thr = warp_min(above < p.k ? best : INFINITY);
-    if (p.bias && thr > -INFINITY) thr -= 2.f * (kSlackAbs + kSlackRel * fabsf(thr));
+    if (p.bias && thr > -INFINITY) thr -= 2.f * kSlackAbs + 2.f * kSlackRel * fabsf(thr);
     __syncwarp();
   }
   int n = 0;
