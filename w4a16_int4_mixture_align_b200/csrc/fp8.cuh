@@ -49,7 +49,6 @@ struct Fp8QuantArgs {
   int64_t max_m;
   uint8_t* q;
   float* scales;
-  int num_sms;
 };
 
 // ---- quantisation of a block (used where rows are quantised and where a product ends in it)

@@ -217,8 +217,7 @@ chord_status_t quantize(const void* x, int dtype, int64_t ld, int64_t rows, int 
   if (!x || !q || !scales) return fail(CHORD_ERR_INVALID_ARG, "null pointer");
   if (misaligned(x, 16) || misaligned(q, 16) || misaligned(scales, 4))
     return fail(CHORD_ERR_INVALID_ARG, "x and q must be 16-byte and scales 4-byte aligned");
-  int num_sms = 0;
-  if ((st = current_device(&num_sms)) != CHORD_OK) return st;
+  if ((st = current_device(nullptr)) != CHORD_OK) return st;
   Fp8QuantArgs a{};
   a.x = x;
   a.dtype = dtype;
@@ -230,7 +229,6 @@ chord_status_t quantize(const void* x, int dtype, int64_t ld, int64_t rows, int 
   a.max_m = masked_m ? rows / E : rows;
   a.q = q;
   a.scales = scales;
-  a.num_sms = num_sms;
   const cudaError_t err = launch_fp8_quantize(a, stream);
   return err == cudaSuccess ? CHORD_OK : cuda_fail(err, "FP8 quantise launch");
 }

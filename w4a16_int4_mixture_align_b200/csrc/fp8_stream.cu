@@ -29,8 +29,6 @@
 //
 // All waits are bounded; on a timeout the CTA raises CHORD_DEV_TIMEOUT, writes nothing more (nor
 // do the others of its cluster), waits (bounded) for what it has in flight and returns.
-#include <mutex>
-
 #include "fp8_tc.cuh"
 
 namespace chord {
