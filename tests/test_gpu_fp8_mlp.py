@@ -88,3 +88,25 @@ def test_status_outlives_growth(chord):  # noqa: F811
     later.fill_(chord.CHORD_DEV_ROUTING_INVALID)
     assert mlp.check_status() == chord.CHORD_DEV_TIMEOUT | chord.CHORD_DEV_ROUTING_INVALID
     assert mlp.check_status() == 0
+
+
+@pytest.mark.parametrize("T,h,i", [(1, 7168, 2048), (16, 7168, 2048), (300, 1024, 512), (2500, 1024, 512)])
+def test_repeats_bit_for_bit(chord, T, h, i):  # noqa: F811
+    """The same call on the same rows gives the same bits, whether its operands come from L2 or HBM."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(T)
+
+    def code(*shape):  # finite codes of both signs
+        return torch.randint(0, 256, shape, generator=g, device="cuda", dtype=torch.uint8).bitwise_and(0xBF)
+
+    mlp = chord.ChordFP8MLP(code(2 * i, h), torch.full((2 * i // 128, h // 128), 0.01, device="cuda"), code(h, i),
+                            torch.full((h // 128, i // 128), 0.01, device="cuda"), max_tokens=T)
+    x = torch.randn((T, h), generator=g, device="cuda").to(torch.bfloat16)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    want = mlp(x)
+    assert torch.isfinite(want.float()).all()
+    for n in range(12):
+        if n % 2:
+            flush.fill_(n)
+        assert torch.equal(mlp(x), want), n
+    assert mlp.check_status() == 0
